@@ -316,6 +316,165 @@ MQ_API mq_status mq_chain_forward(const mq_chain_layer* layers, int n_layers, in
                                   void* scratch, size_t scratch_bytes, int flags, void* stream);
 
 /*
+ * Rotary positions. A head's first rot_dim values are pairs (a, b), rotated at
+ * position p by the angle t = p w_i of pair i:
+ *   (a, b) -> factor (a cos t - b sin t, b cos t + a sin t);
+ * values behind them stay. MQ_ROPE_HALF pairs value i with i + rot_dim / 2,
+ * MQ_ROPE_INTERLEAVED value 2 i with 2 i + 1. turns[i] holds w_i / 2 pi as a
+ * 64-bit fraction of a turn, so the angle at any position is one wrapping
+ * integer product and far positions lose nothing. Negative positions rotate
+ * backwards (the inverse, and with factor 1 the gradient, of the rotation).
+ */
+typedef enum mq_rope_layout { MQ_ROPE_HALF = 0, MQ_ROPE_INTERLEAVED = 1 } mq_rope_layout;
+typedef enum mq_rope_scaling {
+  MQ_ROPE_PLAIN = 0,
+  MQ_ROPE_LINEAR = 1, /* params: factor */
+  MQ_ROPE_BANDS = 2,  /* params: factor, low band, high band, original length */
+  MQ_ROPE_YARN = 3    /* params: factor, beta fast, beta slow, original length */
+} mq_rope_scaling;
+typedef struct mq_rope_positions {
+  const uint64_t* turns; /* rot_dim / 2 (device), 8-byte aligned */
+  int rot_dim;           /* even, at most the head's size */
+  int layout;            /* mq_rope_layout */
+  float factor;
+} mq_rope_positions;
+
+/*
+ * Fills turns (HOST, rot_dim / 2) and factor for base theta: w_i =
+ * theta^(-2 i / rot_dim), scaled for long contexts by
+ *   LINEAR: w / factor;
+ *   BANDS:  pairs that make fewer than `low` turns over the original length
+ *           get w / factor, those above `high` keep w, a blend between;
+ *   YARN (arXiv 2309.00071): a ramp over the pair index between those that
+ *           make beta fast and beta slow turns over the original length, from
+ *           w to w / factor; factor out = 0.1 ln(factor) + 1 (factor > 1).
+ * params: HOST array, as listed at mq_rope_scaling (NULL for PLAIN).
+ */
+MQ_API mq_status mq_rope_table(double theta, int rot_dim, int scaling, const double* params,
+                               uint64_t* turns, float* factor);
+
+/*
+ * Rotates n_rows x n_heads heads of head_dim values: row r's at positions[r].
+ *   x, y : x_dtype / y_dtype (MQ_F32 or MQ_BF16), rows x_stride / y_stride
+ *          ELEMENTS apart (at least n_heads * head_dim), heads dense. y may be
+ *          x (same type and stride); any other overlap is undefined.
+ *   positions : n_rows int32 (device).
+ * fp32 arithmetic, one rounding to y's type. head_dim even, at most 512.
+ * n_rows = 0 does nothing.
+ */
+MQ_API mq_status mq_rope(const void* x, int x_dtype, int64_t n_rows, int64_t n_heads,
+                         int64_t head_dim, int64_t x_stride, const int32_t* positions,
+                         const mq_rope_positions* rope, void* y, int y_dtype, int64_t y_stride,
+                         void* stream);
+
+/*
+ * One layer's paged key/value cache in 8 bits. A page holds page_tokens
+ * consecutive tokens of one sequence; page p, head h of K is the dense tile
+ * k[p][h][token][value] of bytes with the scale k_scale[p][h]:
+ *   value = k_scale[p][h] * (byte - 128),   byte - 128 in [-127, 127].
+ * All pointers device, owned by the caller.
+ */
+typedef struct mq_kv_cache {
+  uint8_t* k;     /* n_pages x n_kv_heads x page_tokens x head_dim, 16-byte aligned */
+  uint8_t* v;     /* the same shape */
+  float* k_scale; /* n_pages x n_kv_heads */
+  float* v_scale;
+  int64_t n_pages;
+  int page_tokens; /* 16, 32, 64 or 128 */
+  int n_kv_heads;  /* at most 1024 */
+  int head_dim;    /* a multiple of 16, at most 256 */
+} mq_kv_cache;
+
+/*
+ * The rows of one call by sequence (ragged). Sequence s owns rows
+ * row_start[s] .. row_start[s + 1] of the call's n_rows row buffers: its newest
+ * tokens. kv_len[s] is its number of tokens with them, so its row i stands at
+ * place kv_len[s] - n + i (n its rows). Token t lies in page
+ * page_table[s * max_pages + t / page_tokens], slot t % page_tokens.
+ * A row whose place is negative is padding: nothing is written to the cache
+ * for it and it attends to nothing (kv_len 0 with one row is an idle slot of a
+ * fixed-size batch). Rows behind row_start[n_seqs] are left as they were.
+ * Device arrays are read on the device: max_new (rows of any sequence) and
+ * max_len (tokens of any sequence) bound them for the launch, and a graph
+ * that captured a call replays with whatever they hold then. A sequence that
+ * does not keep the bounds, or a page number outside [0, n_pages), touches no
+ * memory: mq_device_status() reports MQ_ERR_BOUNDS and the outputs of that
+ * sequence are undefined.
+ */
+typedef struct mq_kv_batch {
+  const int32_t* row_start;  /* n_seqs + 1, not decreasing, row_start[0] >= 0 */
+  const int32_t* kv_len;     /* n_seqs */
+  const int32_t* page_table; /* n_seqs x max_pages */
+  int64_t n_seqs;            /* at most 65535; 0 does nothing */
+  int64_t max_pages;         /* row pitch of page_table */
+  int64_t n_rows;
+  int64_t max_new;
+  int64_t max_len; /* at most max_pages * page_tokens */
+} mq_kv_batch;
+
+/*
+ * Writes the batch's new tokens into the cache, quantised as they are written,
+ * keys rotated first if rope is given; and rotates their queries.
+ * Per page and head, with m = max |x| over the tokens the call adds to it:
+ *   s' = max(s, m / 127)   (s = 0 for a page that held no token before),
+ *   held codes c -> rint(c s / s') where s' > s,   new codes rint(x / s'),
+ * every operation IEEE binary32, correctly rounded (x after rotation in fp32).
+ * A call that repeats tokens writes the same bytes again.
+ *   k, v : n_rows x n_kv_heads x head_dim (MQ_F32 or MQ_BF16), rows k_stride /
+ *          v_stride elements apart (a multiple of 4), aligned to 4 elements;
+ *          finite. A slice of mq_linear's fp32 output will do.
+ *   rope : NULL: no rotation. rot_dim a multiple of 8.
+ *   positions : n_rows int32, or NULL: each row's place in its sequence.
+ *   q    : NULL, or n_rows x n_q_heads x head_dim like k; q_out then receives
+ *          the rotated queries as bf16, dense, 8-byte aligned.
+ * No page may be written for two sequences of one call; a page that sequences
+ * share (a common prefix) must be full.
+ */
+MQ_API mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* k,
+                              const void* v, int dtype, int64_t k_stride, int64_t v_stride,
+                              const mq_rope_positions* rope, const int32_t* positions,
+                              const void* q, int64_t q_stride, int64_t n_q_heads, void* q_out,
+                              void* stream);
+
+/*
+ * Reads tokens back: tokens first[s], first[s] + 1, ... of sequence s become
+ * rows out_start[s] .. out_start[s + 1] of k_out and v_out (n_out rows of
+ * n_kv_heads x head_dim values, dtype MQ_F32 or MQ_BF16, rows out_stride
+ * elements apart, 16-byte aligned). value = scale (byte - 128) in fp32, exact
+ * to one rounding. Rows for tokens at or behind kv_len[s] are left as they were.
+ * max_out bounds the rows of any sequence. The batch's row_start is not used.
+ */
+MQ_API mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                            const int32_t* first, const int32_t* out_start, int64_t n_out,
+                            int64_t max_out, void* k_out, void* v_out, int dtype,
+                            int64_t out_stride, void* stream);
+
+/*
+ * Attention of the batch's rows over their sequences' cached tokens (append
+ * them first): row at place P, query head a, key/value head
+ * h = a / (n_q_heads / n_kv_heads),
+ *   s_j = cap(scale q . k_j),  o = sum_j softmax(s)_j v_j,  lse = ln sum_j e^{s_j}
+ * over j <= P (and j > P - window if window > 0), cap(s) = softcap
+ * tanh(s / softcap) if softcap > 0. A row that sees no token gets o = 0 and
+ * lse = -infinity. What pages hold behind kv_len has no part in it.
+ *   q, out : n_rows x n_q_heads x head_dim bf16, rows q_stride / out_stride
+ *            elements apart (multiples of 8), 16-byte aligned, not overlapping.
+ *   lse    : n_rows x n_q_heads fp32, or NULL.
+ *   scratch: mq_kv_attention_scratch_bytes (device), 256-byte aligned, owned by
+ *            the caller; calls that overlap on the GPU need one each. It need
+ *            not be cleared and keeps nothing for the next call.
+ * Any number of rows: single tokens, drafted tokens and prompts may share a
+ * call. fp32 sums and statistics; probabilities are rounded to fp16 before
+ * they weigh V. Results do not depend on timing.
+ */
+MQ_API size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                                            int64_t n_q_heads);
+MQ_API mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q,
+                                 int64_t q_stride, int64_t n_q_heads, float scale, float softcap,
+                                 int64_t window, void* out, int64_t out_stride, float* lse,
+                                 void* scratch, size_t scratch_bytes, void* stream);
+
+/*
  * The int8 container as a file: the one stored artifact, from which every
  * width is sliced. Host buffers (the caller copies device data). Layout,
  * little-endian: "MQC8", version 1 (uint32), N, K (int64), q (N x K uint8,

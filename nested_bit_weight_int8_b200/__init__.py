@@ -45,6 +45,25 @@ class ChainLayer(ctypes.Structure):
 
 
 MQ_CHAIN_GRAPH = 1
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"plain": (0, 0), "linear": (1, 1), "bands": (2, 4), "yarn": (3, 4)}  # code, params
+
+
+class RopePositions(ctypes.Structure):
+    """mq_rope_positions: the rotary table and layout."""
+    _fields_ = [("turns", _vp), ("rot_dim", _int), ("layout", _int), ("factor", ctypes.c_float)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """mq_kv_cache: one layer's paged 8-bit cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("n_pages", _i64),
+                ("page_tokens", _int), ("n_kv_heads", _int), ("head_dim", _int)]
+
+
+class KVBatchDesc(ctypes.Structure):
+    """mq_kv_batch: the rows of one call by sequence."""
+    _fields_ = [("row_start", _vp), ("kv_len", _vp), ("page_table", _vp), ("n_seqs", _i64),
+                ("max_pages", _i64), ("n_rows", _i64), ("max_new", _i64), ("max_len", _i64)]
 
 
 def _sig(name, res, args):
@@ -82,6 +101,19 @@ _chain_views = _sig("mq_chain_scratch_views", _int, [_i64, _i64, _i64, _i64, cty
 _chain = _sig("mq_chain_forward", _int,
               [ctypes.POINTER(ChainLayer), _int, _i64, _i64, _i64, _i64, _i64, _vp, _vp,
                ctypes.c_size_t, _int, _vp])
+_cacheP, _batchP, _ropeP = (ctypes.POINTER(t) for t in (KVCacheDesc, KVBatchDesc, RopePositions))
+_rope_table = _sig("mq_rope_table", _int,
+                   [ctypes.c_double, _int, _int, ctypes.POINTER(ctypes.c_double), _vp,
+                    ctypes.POINTER(ctypes.c_float)])
+_rope = _sig("mq_rope", _int, [_vp, _int, _i64, _i64, _i64, _i64, _vp, _ropeP, _vp, _int, _i64, _vp])
+_kv_append = _sig("mq_kv_append", _int,
+                  [_cacheP, _batchP, _vp, _vp, _int, _i64, _i64, _ropeP, _vp, _vp, _i64, _i64, _vp, _vp])
+_kv_read = _sig("mq_kv_read", _int,
+                [_cacheP, _batchP, _vp, _vp, _i64, _i64, _vp, _vp, _int, _i64, _vp])
+_kv_scratch = _sig("mq_kv_attention_scratch_bytes", ctypes.c_size_t, [_cacheP, _batchP, _i64])
+_kv_attention = _sig("mq_kv_attention", _int,
+                     [_cacheP, _batchP, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float, _i64, _vp,
+                      _i64, _vp, _vp, ctypes.c_size_t, _vp])
 _c_save = _sig("mq_container_save", _int, [ctypes.c_char_p, _vp, _vp, _vp, _i64, _i64])
 _c_info = _sig("mq_container_info", _int,
                [ctypes.c_char_p, ctypes.POINTER(_i64), ctypes.POINTER(_i64)])
@@ -99,7 +131,8 @@ EXPORTED = ("mq_version", "mq_last_error", "mq_packed_bytes", "mq_quantize_int8"
             "mq_quantize_int8_clipped", "mq_linear_container", "mq_ep_overflow_rows",
             "mq_ep_overflow_cols", "mq_linear_ep", "mq_chain_scratch_bytes",
             "mq_chain_forward", "mq_container_save", "mq_container_info", "mq_container_load",
-            "mq_chain_scratch_views", "mq_debug_map_table_count")
+            "mq_chain_scratch_views", "mq_debug_map_table_count", "mq_rope_table", "mq_rope",
+            "mq_kv_append", "mq_kv_read", "mq_kv_attention_scratch_bytes", "mq_kv_attention")
 
 NOALLOC_SCRATCH_BYTES = 1280 * 1024
 
@@ -224,6 +257,102 @@ class ChainPlan:
         nbytes = scratch.numel() * scratch.element_size()
         _check(_chain(self.arr, self.n, self.M, self.D, self.Dkv, self.F, self.hd, _ptr(h),
                       _ptr(scratch), nbytes, MQ_CHAIN_GRAPH if graph else 0, _stream(stream)))
+
+
+class RopeTable:
+    """Rotary positions for heads of which the first rot_dim values turn:
+    base theta, layout "half" or "interleaved", scaling "plain", "linear"
+    (params: factor), "bands" (factor, low, high, original length) or "yarn"
+    (factor, beta fast, beta slow, original length). Holds the device table."""
+
+    def __init__(self, theta: float, rot_dim: int, layout: str = "half", scaling: str = "plain",
+                 params=(), device=None):
+        import torch
+        code, n = ROPE_SCALINGS[scaling]
+        if len(params) != n:
+            raise ValueError(f"{scaling} scaling takes {n} parameters")
+        host = torch.zeros(max(rot_dim // 2, 1), dtype=torch.int64)
+        factor = ctypes.c_float(0)
+        _check(_rope_table(theta, rot_dim, code, (ctypes.c_double * max(n, 1))(*params), host.data_ptr(),
+                           ctypes.byref(factor)))
+        self.turns = host if device is None else host.to(device)
+        self.factor = factor.value
+        self.desc = RopePositions(self.turns.data_ptr(), rot_dim, ROPE_LAYOUTS[layout], factor.value)
+
+
+class KVCache:
+    """One layer's paged 8-bit cache over the caller's tensors: k, v
+    (pages, kv heads, page tokens, head dim) uint8, scales (pages, kv heads)
+    fp32, all dense. The descriptor is marshalled once."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        pages, heads, page, dim = k.shape
+        for t, shape, item in ((k, k.shape, 1), (v, k.shape, 1), (k_scale, (pages, heads), 4),
+                               (v_scale, (pages, heads), 4)):
+            if tuple(t.shape) != tuple(shape) or t.element_size() != item or not t.is_contiguous():
+                raise ValueError("cache tensors must be dense: codes (pages, heads, page, dim) uint8, "
+                                 "scales (pages, heads) fp32")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                                page, heads, dim)
+
+
+class KVBatch:
+    """The rows of one call by sequence, over the caller's int32 tensors:
+    row_start (seqs + 1), kv_len (seqs), page_table (seqs, max pages). max_new
+    and max_len bound the rows and tokens of any sequence."""
+
+    def __init__(self, row_start, kv_len, page_table, n_rows: int, max_new: int, max_len: int):
+        seqs = kv_len.shape[0]
+        for t, shape in ((row_start, (seqs + 1,)), (kv_len, (seqs,)), (page_table, (seqs, page_table.shape[-1]))):
+            if tuple(t.shape) != shape or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+                raise ValueError("batch tensors must be dense int32: row_start (seqs + 1), kv_len (seqs), "
+                                 "page_table (seqs, pages)")
+        self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table
+        self.desc = KVBatchDesc(row_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs,
+                                page_table.shape[1], n_rows, max_new, max_len)
+
+
+def rope(x, x_dtype: int, n_rows: int, n_heads: int, head_dim: int, x_stride: int, positions, table: RopeTable,
+         y, y_dtype: int, y_stride: int, stream=None) -> None:
+    """Rotary positions of n_rows x n_heads heads; y may be x. Strides in elements."""
+    _check(_rope(_ptr(x), x_dtype, n_rows, n_heads, head_dim, x_stride, _ptr(positions), table.desc, _ptr(y),
+                 y_dtype, y_stride, _stream(stream)))
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, dtype: int, k_stride: int, v_stride: int,
+              rope: RopeTable | None = None, positions=None, q=None, q_stride: int = 0, n_q_heads: int = 0,
+              q_out=None, stream=None) -> None:
+    """Quantises the batch's new keys (rotated) and values into the cache, and
+    writes their rotated queries to q_out (bf16) if q is given."""
+    _check(_kv_append(cache.desc, batch.desc, _ptr(k), _ptr(v), dtype, k_stride, v_stride,
+                      rope.desc if rope is not None else None, _ptr(positions), _ptr(q), q_stride, n_q_heads,
+                      _ptr(q_out), _stream(stream)))
+
+
+def kv_read(cache: KVCache, batch: KVBatch, first, out_start, n_out: int, max_out: int, k_out, v_out,
+            dtype: int, out_stride: int, stream=None) -> None:
+    """Reads the cached tokens first[s], first[s] + 1, ... of each sequence into
+    rows out_start[s] .. out_start[s + 1] of k_out and v_out."""
+    _check(_kv_read(cache.desc, batch.desc, _ptr(first), _ptr(out_start), n_out, max_out, _ptr(k_out),
+                    _ptr(v_out), dtype, out_stride, _stream(stream)))
+
+
+def kv_attention_scratch_bytes(cache: KVCache, batch: KVBatch, n_q_heads: int) -> int:
+    n = int(_kv_scratch(cache.desc, batch.desc, n_q_heads))
+    if n == 0:
+        raise MQError(MQ_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, q, q_stride: int, n_q_heads: int, scale: float, out,
+                 out_stride: int, scratch, lse=None, softcap: float = 0.0, window: int = 0, stream=None) -> None:
+    """Attention of the batch's rows (bf16 q) over the cached tokens of their
+    sequences, causal by their places; out bf16, lse (n_rows x n_q_heads fp32)
+    if given. scratch: kv_attention_scratch_bytes."""
+    _check(_kv_attention(cache.desc, batch.desc, _ptr(q), q_stride, n_q_heads, scale, softcap, window, _ptr(out),
+                         out_stride, _ptr(lse), _ptr(scratch), scratch.numel() * scratch.element_size(),
+                         _stream(stream)))
 
 
 def save_container(path: str, q, alpha, zero) -> None:

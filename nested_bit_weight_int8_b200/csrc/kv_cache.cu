@@ -1,0 +1,464 @@
+// Rotary positions, the quantising write of the 8-bit key/value cache and its
+// read-back.
+//
+// Rotary positions: pair i of a head, (a, b), at position p becomes
+//   f (a cos t - b sin t, b cos t + a sin t),   t = p w_i,
+// with w_i the pair's angle per position and f a factor. The caller's table
+// holds w_i / 2 pi as a 64-bit fraction of a turn, so p w_i modulo one turn is
+// one wrapping integer product, exact to 2^-64 turns times p at any position;
+// only the reduced angle becomes fp32.
+//
+// The cache: a page and head of K (or V) holds codes c in [-127, 127] as bytes
+// c + 128 and one scale s, value = s c. A call that adds tokens to a page sets
+//   s' = max(s_old if the page held tokens before, max |x_new| / 127),
+// rounds what the page held to the new scale, c' = rint(c s_old / s'), where
+// it grew, and writes rint(x / s'). Every operation is IEEE binary32, correctly
+// rounded, so equal inputs give equal bytes.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/mq.h"
+#include "kv_internal.h"
+#include "mq_device.cuh"
+#include "mq_internal.h"
+
+namespace mq {
+namespace {
+
+// cos and sin of 2 pi phase / 2^64. The nearest quarter turn is split off in
+// integers; the rest, |x| <= pi / 4, goes through the Taylor series (last terms
+// below 2^-31). Rounding x costs 2 u of 0.79 (u = 2^-24) and the last sums one,
+// so both are within 3 u of the value.
+__device__ __forceinline__ void turn_sincos(uint64_t phase, float& sn, float& cs) {
+  const uint32_t top = static_cast<uint32_t>(phase >> 32);
+  const uint32_t quarter = (top + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(top - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, 1/7!
+  s = fmaf(z, s, 8.3333333e-3f);
+  s = fmaf(z, s, -1.6666667e-1f);
+  s = fmaf(z * x, s, x);
+  float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);  // 1/10!, 1/8!
+  c = fmaf(z, c, -1.3888889e-3f);
+  c = fmaf(z, c, 4.1666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  const float a = (quarter & 1) ? c : s, b = (quarter & 1) ? s : c;
+  sn = (quarter & 2) ? -a : a;
+  cs = ((quarter + 1) & 2) ? -b : b;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
+  if constexpr (V == 4 && sizeof(T) == 4) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else if constexpr (V == 4) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = __uint_as_float(u.x << 16);
+    v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(u.y << 16);
+    v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = static_cast<float>(p[i]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+  if constexpr (V == 4 && sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = static_cast<T>(v[i]);
+  }
+}
+
+// A head's d values are cut into d / (2 V) units of two runs of V values. Units
+// below rot / (2 V) hold V pairs: runs u V and u V + rot / 2 (half layout), or
+// 2 u V and 2 u V + V (interleaved: the pairs lie next to one another). The
+// others, behind the rotated part, are plain.
+struct Unit {
+  int c0, c1;
+  bool turned;
+};
+template <int V>
+__device__ __forceinline__ Unit unit_of(int u, int rot, bool interleaved) {
+  const bool turned = u * 2 * V < rot;
+  if (turned && !interleaved) return Unit{u * V, u * V + (rot >> 1), true};
+  return Unit{u * 2 * V, u * 2 * V + V, turned};
+}
+// Index of the first of a turned unit's V frequencies: pair u V + i.
+template <int V>
+__device__ __forceinline__ void unit_angles(const Rope& r, int u, int pos, float (&sn)[V], float (&cs)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    turn_sincos(r.turns[u * V + i] * static_cast<uint64_t>(static_cast<int64_t>(pos)), sn[i], cs[i]);
+    sn[i] *= r.factor;
+    cs[i] *= r.factor;
+  }
+}
+template <int V>
+__device__ __forceinline__ void unit_turn(bool interleaved, float (&a)[V], float (&b)[V], const float (&sn)[V],
+                                          const float (&cs)[V]) {
+  if (!interleaved || V == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float x = a[i], y = b[i];
+      a[i] = fmaf(x, cs[i], -(y * sn[i]));
+      b[i] = fmaf(y, cs[i], x * sn[i]);
+    }
+  } else {
+    // run a holds pairs 0 .. V/2 - 1, run b the others
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float x = a[2 * i], y = a[2 * i + 1];
+      a[2 * i] = fmaf(x, cs[i], -(y * sn[i]));
+      a[2 * i + 1] = fmaf(y, cs[i], x * sn[i]);
+      const float w = b[2 * i], z = b[2 * i + 1];
+      b[2 * i] = fmaf(w, cs[V / 2 + i], -(z * sn[V / 2 + i]));
+      b[2 * i + 1] = fmaf(z, cs[V / 2 + i], w * sn[V / 2 + i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ rotary
+constexpr int kRopeThreads = 256;
+
+// One CTA per (row, share of its heads): thread (head lane, unit) forms its
+// unit's cosines once and walks the heads with them. Each value is read once
+// and written once, both runs of a unit before either is written, so y may be
+// x. V = 4 needs rot and d in eights and aligned runs; V = 1 takes the rest.
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const TI* x, int64_t rows, int heads, int d, int64_t x_stride, const int32_t* __restrict__ positions,
+            Rope rope, TO* y, int64_t y_stride, int units, int head_lanes, int head_splits) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int u = threadIdx.x % units, hl = threadIdx.x / units;
+  if (hl >= head_lanes) return;
+  const Unit un = unit_of<V>(u, rope.rot, rope.interleaved != 0);
+  const int part = blockIdx.x % head_splits;
+  for (int64_t r = blockIdx.x / head_splits; r < rows; r += gridDim.x / head_splits) {
+    float sn[V], cs[V];
+    if (un.turned) unit_angles<V>(rope, u, positions[r], sn, cs);
+    for (int h = part * head_lanes + hl; h < heads; h += head_splits * head_lanes) {
+      const TI* xr = x + r * x_stride + int64_t(h) * d;
+      TO* yr = y + r * y_stride + int64_t(h) * d;
+      float a[V], b[V];
+      load_v<TI, V>(xr + un.c0, a);
+      load_v<TI, V>(xr + un.c1, b);
+      if (un.turned) unit_turn<V>(rope.interleaved != 0, a, b, sn, cs);
+      store_v<TO, V>(yr + un.c0, a);
+      store_v<TO, V>(yr + un.c1, b);
+    }
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t rope_typed(const void* x, int64_t rows, int heads, int d, int64_t x_stride, const int32_t* positions,
+                       const Rope& rope, void* y, int64_t y_stride, cudaStream_t stream, int sms) {
+  auto run_ok = [](const void* p, int64_t stride, int item) {
+    return (reinterpret_cast<uintptr_t>(p) % (4 * item)) == 0 && stride % 4 == 0;
+  };
+  const bool wide = rope.rot % 8 == 0 && d % 8 == 0 && run_ok(x, x_stride, sizeof(TI)) && run_ok(y, y_stride, sizeof(TO));
+  const int units = wide ? d / 8 : d / 2;
+  int head_lanes = kRopeThreads / units;
+  if (head_lanes < 1) return cudaErrorNotSupported;
+  if (head_lanes > heads) head_lanes = heads;
+  // few rows: the heads of a row are shared out so that the card fills
+  int splits = static_cast<int>((4 * int64_t(sms) + rows - 1) / rows);
+  const int most = (heads + head_lanes - 1) / head_lanes;
+  splits = splits < 1 ? 1 : (splits > most ? most : splits);
+  int64_t grid = rows * splits;
+  const int64_t cap = (int64_t(1) << 30) / splits * splits;
+  if (grid > cap) grid = cap;
+  const int threads = (units * head_lanes + 31) / 32 * 32;
+  if (wide)
+    return launch_pdl(rope_kernel<TI, TO, 4>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, stream,
+                      static_cast<const TI*>(x), rows, heads, d, x_stride, positions, rope, static_cast<TO*>(y), y_stride,
+                      units, head_lanes, splits);
+  return launch_pdl(rope_kernel<TI, TO, 1>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, stream,
+                    static_cast<const TI*>(x), rows, heads, d, x_stride, positions, rope, static_cast<TO*>(y), y_stride,
+                    units, head_lanes, splits);
+}
+
+// ------------------------------------------------------------------ append
+// The sequence that holds `row`, found by the warp 32 candidates at a time:
+// the largest s with row_start[s] <= row, or -1 for a row behind the last.
+__device__ __forceinline__ int find_seq(const KvBatch& b, int row, int lane) {
+  if (row >= b.row_start[b.n_seqs]) return -1;
+  int lo = 0, n = b.n_seqs;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const bool ok = lane * step < n && b.row_start[i] <= row;
+    const unsigned hit = __ballot_sync(0xffffffffu, ok);
+    const int last = 31 - __clz(hit | 1u);
+    const int end = lo + n;
+    lo += last * step;
+    n = min(step, end - lo);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float scale) {
+  // finite x: |x / scale| <= 127 up to a rounding; the clamp also gives a
+  // defined byte to what is not finite
+  const float t = scale > 0.f ? rintf(__fdiv_rn(x, scale)) : 0.f;
+  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(t, -127.f), 127.f)) + 128);
+}
+
+constexpr int kUnitsPerThread = 4;
+
+// CTAs below kv_blocks: one page of one sequence, one head, K or V. The new
+// values of the page stay in registers (at most 4 units of 8 a thread) from
+// the maximum to the bytes, so they are read once. The others: the queries,
+// one row and a share of its heads each.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int d = a.c.d, units = d >> 3;
+  const bool il = a.rope.interleaved != 0;
+  if (static_cast<int>(blockIdx.x) >= kv_blocks) {
+    const int i = blockIdx.x - kv_blocks;
+    const int row = i / q_splits;
+    int pos = 0;
+    if (a.rope.turns) {
+      if (a.positions) {
+        pos = a.positions[row];
+        if (row >= a.b.row_start[a.b.n_seqs]) return;
+      } else {
+        const int s = find_seq(a.b, row, lane);
+        if (s < 0) return;
+        pos = a.b.kv_len[s] - a.b.row_start[s + 1] + row;
+      }
+    } else if (row >= a.b.row_start[a.b.n_seqs]) {
+      return;
+    }
+    const int head_lanes = blockDim.x / units;
+    const int u = tid % units, hl = tid / units;
+    if (hl >= head_lanes) return;
+    const Unit un = unit_of<4>(u, a.rope.turns ? a.rope.rot : 0, il);
+    float sn[4], cs[4];
+    if (un.turned) unit_angles<4>(a.rope, u, pos, sn, cs);
+    for (int h = (i % q_splits) * head_lanes + hl; h < a.n_q_heads; h += q_splits * head_lanes) {
+      const T* x = static_cast<const T*>(a.q) + row * a.q_stride + int64_t(h) * d;
+      float p[4], q[4];
+      load_v<T, 4>(x + un.c0, p);
+      load_v<T, 4>(x + un.c1, q);
+      if (un.turned) unit_turn<4>(il, p, q, sn, cs);
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.q_out) + (int64_t(row) * a.n_q_heads + h) * d;
+      store_v<__nv_bfloat16, 4>(o + un.c0, p);
+      store_v<__nv_bfloat16, 4>(o + un.c1, q);
+    }
+    return;
+  }
+  __shared__ float s_max[32];
+  int i = blockIdx.x;
+  const bool is_v = i & 1;
+  i >>= 1;
+  const int h = i % a.c.heads;
+  i /= a.c.heads;
+  const int slot_page = i % page_slots, s = i / page_slots;
+  const Seq sq = load_seq(a.b, s, (is_v || h || slot_page) ? nullptr : a.err);
+  const int start = max(sq.len - sq.n, 0);  // first new token
+  const int index = (start >> a.c.page_log2) + slot_page;
+  const int base = index << a.c.page_log2;
+  if (sq.n == 0 || base >= sq.len) return;
+  const int lo = max(start - base, 0), hi = min(sq.len - base, a.c.page);  // new tokens of the page
+  const int pid = load_page(a.c, a.b, s, index, a.err);
+  if (pid < 0) return;
+  const int64_t tile = int64_t(pid) * a.c.heads + h;
+  float* scale_p = (is_v ? a.c.v_scale : a.c.k_scale) + tile;
+  uint8_t* codes = (is_v ? a.c.v : a.c.k) + tile * a.c.page * d;
+  const float old = lo > 0 ? *scale_p : 0.f;
+  // row of the page's token t: r0 + (base + t) - (len - n)
+  const int64_t row0 = sq.r0 + int64_t(base) - (sq.len - sq.n);
+  const T* x = static_cast<const T*>(is_v ? a.v : a.k);
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const bool turn = a.rope.turns && !is_v;
+  const int total = (hi - lo) * units;
+  float va[kUnitsPerThread][4], vb[kUnitsPerThread][4];
+  float mx = 0.f;
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int w = tid + k * blockDim.x;
+    if (w < total) {
+      const int u = w % units;
+      const int64_t row = row0 + lo + w / units;
+      const Unit un = unit_of<4>(u, turn ? a.rope.rot : 0, il);
+      const T* xr = x + row * stride + int64_t(h) * d;
+      load_v<T, 4>(xr + un.c0, va[k]);
+      load_v<T, 4>(xr + un.c1, vb[k]);
+      if (un.turned) {
+        float sn[4], cs[4];
+        const int pos = a.positions ? a.positions[row] : base + lo + w / units;
+        unit_angles<4>(a.rope, u, pos, sn, cs);
+        unit_turn<4>(il, va[k], vb[k], sn, cs);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(va[k][e]), fabsf(vb[k][e])));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  if (blockDim.x > 32) {
+    if (lane == 0) s_max[tid >> 5] = mx;
+    __syncthreads();
+    mx = lane < static_cast<int>(blockDim.x >> 5) ? s_max[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  const float scale = fmaxf(old, __fdiv_rn(mx, 127.f));
+  if (lo > 0 && scale > old) {
+    // the scale grew: what the page held is rounded to it
+    for (int w = tid; w < lo * d / 16; w += blockDim.x) {
+      uint4* p = reinterpret_cast<uint4*>(codes) + w;
+      uint4 c = *p;
+      uint32_t* cw = &c.x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t r = 0;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float v = static_cast<float>(static_cast<int>((cw[e] >> (8 * f)) & 255u) - 128);
+          r |= code_of(__fmul_rn(v, old), scale) << (8 * f);
+        }
+        cw[e] = r;
+      }
+      *p = c;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int w = tid + k * blockDim.x;
+    if (w < total) {
+      const Unit un = unit_of<4>(w % units, turn ? a.rope.rot : 0, il);
+      uint8_t* o = codes + (lo + w / units) * d;
+      uint32_t p = 0, q = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        p |= code_of(va[k][e], scale) << (8 * e);
+        q |= code_of(vb[k][e], scale) << (8 * e);
+      }
+      *reinterpret_cast<uint32_t*>(o + un.c0) = p;
+      *reinterpret_cast<uint32_t*>(o + un.c1) = q;
+    }
+  }
+  if (tid == 0) *scale_p = scale;
+}
+
+// ------------------------------------------------------------------ read
+constexpr int kReadThreads = 128;
+
+// One CTA per (page of a sequence's range, head, K or V): bytes in, values
+// out, 16 bytes of output a thread and step.
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads)
+kv_read_kernel(const ReadArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  constexpr int V = 16 / sizeof(T);
+  const int s = blockIdx.z, h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const int o0 = a.out_start[s];
+  int n = a.out_start[s + 1] - o0;
+  const int first = a.first[s];
+  const int len = a.b.kv_len[s];
+  if (o0 < 0 || n < 0 || n > a.max_out || o0 > a.n_out - n || first < 0 || len > a.b.max_len) {
+    if (threadIdx.x == 0) atomicOr(a.err, kErrBounds);
+    return;
+  }
+  n = min(n, len - first);  // rows for tokens that the sequence does not hold stay as they were
+  const int index = (first >> a.c.page_log2) + blockIdx.x;
+  const int base = index << a.c.page_log2;
+  const int lo = max(first - base, 0), hi = min(first + n - base, a.c.page);
+  if (n <= 0 || lo >= hi) return;
+  const int pid = load_page(a.c, a.b, s, index, a.err);
+  if (pid < 0) return;
+  const int d = a.c.d;
+  const int64_t tile = int64_t(pid) * a.c.heads + h;
+  const float scale = (is_v ? a.c.v_scale : a.c.k_scale)[tile];
+  const uint8_t* codes = (is_v ? a.c.v : a.c.k) + tile * a.c.page * d;
+  T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + (int64_t(o0) + base - first) * a.out_stride + int64_t(h) * d;
+  const int per_row = d / V;
+  for (int w = lo * per_row + threadIdx.x; w < hi * per_row; w += kReadThreads) {
+    const int t = w / per_row, c = (w - t * per_row) * V;
+    float v[V];
+    uint32_t u[V / 4];
+    if constexpr (V == 8) {
+      const uint2 g = *reinterpret_cast<const uint2*>(codes + t * d + c);
+      u[0] = g.x;
+      u[1] = g.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(codes + t * d + c);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      v[e] = __fmul_rn(scale, static_cast<float>(static_cast<int>((u[e / 4] >> (8 * (e % 4))) & 255u) - 128));
+    T* o = out + t * a.out_stride + c;
+    if constexpr (V == 8) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void* x, int x_dtype, int64_t rows, int heads, int d, int64_t x_stride,
+                        const int32_t* positions, const Rope& rope, void* y, int y_dtype, int64_t y_stride,
+                        cudaStream_t stream, int sms) {
+  if (x_dtype == MQ_F32 && y_dtype == MQ_F32)
+    return rope_typed<float, float>(x, rows, heads, d, x_stride, positions, rope, y, y_stride, stream, sms);
+  if (x_dtype == MQ_F32)
+    return rope_typed<float, __nv_bfloat16>(x, rows, heads, d, x_stride, positions, rope, y, y_stride, stream, sms);
+  if (y_dtype == MQ_F32)
+    return rope_typed<__nv_bfloat16, float>(x, rows, heads, d, x_stride, positions, rope, y, y_stride, stream, sms);
+  return rope_typed<__nv_bfloat16, __nv_bfloat16>(x, rows, heads, d, x_stride, positions, rope, y, y_stride, stream, sms);
+}
+
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream) {
+  const int units = a.c.d / 8;
+  const int tokens = a.b.max_new < a.c.page ? a.b.max_new : a.c.page;
+  int threads = 32;  // every unit of a page in registers: at most 4 a thread
+  while (threads < 1024 && threads * kUnitsPerThread < tokens * units) threads *= 2;
+  const int page_slots = (a.b.max_new + a.c.page - 2) / a.c.page + 1;
+  const int64_t kv_blocks = int64_t(a.b.n_seqs) * page_slots * a.c.heads * 2;
+  int q_splits = 0;
+  if (a.q) {
+    const int head_lanes = threads / units;  // d <= 256: at most 32 units
+    q_splits = (a.n_q_heads + head_lanes - 1) / head_lanes;
+  }
+  const int64_t grid = kv_blocks + int64_t(a.b.n_rows) * q_splits;
+  if (grid > 0x7fffffff) return cudaErrorNotSupported;
+  const dim3 g(static_cast<unsigned>(grid)), t(threads);
+  if (dtype == MQ_F32)
+    return launch_pdl(kv_append_kernel<float>, g, t, 0, stream, a, page_slots, static_cast<int>(kv_blocks), q_splits);
+  return launch_pdl(kv_append_kernel<__nv_bfloat16>, g, t, 0, stream, a, page_slots, static_cast<int>(kv_blocks), q_splits);
+}
+
+cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream) {
+  const int slots = (a.max_out + a.c.page - 2) / a.c.page + 1;
+  if (a.c.heads * 2 > 65535 || a.b.n_seqs > 65535) return cudaErrorNotSupported;
+  const dim3 g(slots, a.c.heads * 2, a.b.n_seqs);
+  if (dtype == MQ_F32) return launch_pdl(kv_read_kernel<float>, g, dim3(kReadThreads), 0, stream, a);
+  return launch_pdl(kv_read_kernel<__nv_bfloat16>, g, dim3(kReadThreads), 0, stream, a);
+}
+
+}  // namespace mq

@@ -1,0 +1,126 @@
+// The paged 8-bit key/value cache and the rotary positions as the kernels see
+// them (kv_cache.cu, kv_attention.cu), and the launchers behind the entry
+// points of kv_api.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace mq {
+
+// One layer's cache: pages of `page` tokens, each page and key/value head one
+// contiguous tile of page x d bytes (byte = code + 128) with one fp32 scale.
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;  // n_pages x heads
+  float* v_scale;
+  int n_pages;
+  int page;      // tokens per page: 16, 32, 64 or 128
+  int page_log2;
+  int heads;
+  int d;
+};
+
+// The rows of one call, by sequence (device arrays).
+struct KvBatch {
+  const int32_t* row_start;  // n_seqs + 1
+  const int32_t* kv_len;     // n_seqs, the new rows included
+  const int32_t* pages;      // n_seqs x max_pages
+  int n_seqs;
+  int max_pages;
+  int n_rows;
+  int max_new;
+  int max_len;
+};
+
+// Rotary positions: angle of pair i at position p = 2 pi frac(p turns[i] / 2^64).
+struct Rope {
+  const uint64_t* turns;  // rot / 2; null: no rotation
+  int rot;
+  int interleaved;
+  float factor;
+};
+
+struct AppendArgs {
+  KvCache c;
+  KvBatch b;
+  Rope rope;
+  const void* k;
+  const void* v;
+  const void* q;       // null: no queries
+  int64_t k_stride, v_stride, q_stride;  // elements between rows
+  const int32_t* positions;              // null: a token's place in its sequence
+  uint16_t* q_out;     // n_rows x n_q_heads x d bf16
+  int n_q_heads;
+  uint32_t* err;
+};
+
+struct ReadArgs {
+  KvCache c;
+  KvBatch b;
+  const int32_t* first;      // n_seqs
+  const int32_t* out_start;  // n_seqs + 1
+  int n_out, max_out;
+  void* k_out;
+  void* v_out;
+  int64_t out_stride;
+  uint32_t* err;
+};
+
+struct AttendArgs {
+  KvCache c;
+  KvBatch b;
+  const uint16_t* q;  // bf16
+  int64_t q_stride;
+  int group;          // query heads per key/value head
+  float scale;
+  float softcap;      // 0: none
+  int window;         // 0: none
+  uint16_t* out;      // bf16
+  int64_t out_stride;
+  float* lse;         // n_rows x (heads * group), or null
+  uint8_t* scratch;
+  uint32_t* err;
+};
+
+cudaError_t launch_rope(const void* x, int x_dtype, int64_t rows, int heads, int d, int64_t x_stride,
+                        const int32_t* positions, const Rope& rope, void* y, int y_dtype, int64_t y_stride,
+                        cudaStream_t stream, int sms);
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream);
+size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
+cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms);
+
+#ifdef __CUDACC__
+// A sequence of the batch: its first row, its rows and its tokens. A sequence
+// whose numbers do not fit the call (rows outside [0, n_rows), more rows than
+// max_new, more tokens than max_len) is flagged and has no rows.
+struct Seq {
+  int r0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const KvBatch& b, int s, uint32_t* err) {
+  Seq q;
+  q.r0 = b.row_start[s];
+  q.n = b.row_start[s + 1] - q.r0;
+  q.len = b.kv_len[s];
+  if (q.r0 < 0 || q.n < 0 || q.n > b.max_new || q.r0 > b.n_rows - q.n || q.len > b.max_len) {
+    if (err) atomicOr(err, 16u);  // kErrBounds
+    q.n = 0;
+    q.len = 0;
+  }
+  q.len = q.len < 0 ? 0 : q.len;
+  return q;
+}
+// The page that holds token `index * page` of sequence s, or -1 (flagged)
+// where the table names none.
+__device__ __forceinline__ int load_page(const KvCache& c, const KvBatch& b, int s, int index, uint32_t* err) {
+  const int p = b.pages[int64_t(s) * b.max_pages + index];
+  if (p >= 0 && p < c.n_pages) return p;
+  atomicOr(err, 16u);
+  return -1;
+}
+#endif
+
+}  // namespace mq
