@@ -9,17 +9,26 @@
 // byte read. The token axis of all items together is cut into equal ranges,
 // one per warp of the card; ragged lengths balance by themselves and one
 // long sequence fills every SM. A warp streams its range through its own ring
-// of shared memory (cp.async, 16 bytes), with no barrier between warps. An item
-// that several warps share leaves partial sums that a second kernel joins, in a
-// fixed order, so results do not depend on timing.
+// of shared memory (TMA boxes of 16 tokens, swizzled), with no barrier between
+// warps. Pieces of an item are joined within the CTA first, then, by a second
+// kernel, over the CTAs; always in their order, so results do not depend on
+// timing.
 //
-// Arithmetic: bytes become fp16 exactly (0x6400 | byte is 1024 + byte; minus
-// 1152), m16n8k16 products with fp32 sums. A query row (bf16) is scaled by a
-// power of two to below 2 first, so fp16 holds it exactly down to 2^-24 of the
-// row's largest value. Probabilities are rounded to fp16 (2^-12 of each; they
-// are scaled by 2^14, so those down to 2^-28 of the row's largest keep that),
-// with the page's V scale relative to the largest seen folded in before. The
-// sums of exponentials stay fp32 and unrounded.
+// Arithmetic: S^T = K Q^T and O^T = V^T P^T in m16n8k16 products with fp32 sums,
+// the tokens (then the values of a head) on the 16 side and 8 query rows on the
+// other: one product takes 256 bytes of the cache, and a tile of up to 8 rows
+// wastes nothing on padding. A byte b enters as the fp16 subnormal b 2^-24, which
+// takes one byte permutation per two values and no arithmetic; the offset 128
+// comes out of the sums: scores start at -128 2^-24 sum(q), and one more product
+// sums the probabilities that the outputs' 128 stands against. A query row (bf16)
+// is scaled by a power of two to below 2 first, so fp16 holds it exactly down to
+// 2^-24 of the row's largest value. Probabilities are rounded to fp16 (2^-11 of
+// each), with the page's V scale relative to the largest seen folded in before;
+// they stand 2^8 high, and the running maximum is raised only when a score passes
+// it by 6 (base 2), so they stay below 2^14, keep their precision down to 2^-22 of
+// the maximum and lose at most 2^-33 of it below. The sums of exponentials stay
+// fp32 and unrounded.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,11 +43,13 @@
 namespace mq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPScale = 16384.f;  // 2^14
+constexpr float kPScale = 256.f;
+constexpr float kSlack = 6.f;  // base 2
+constexpr float kCode = 0x1p-24f;
+// V scales below this count as this (what it would gain, fp32 could not hold)
+constexpr float kTinyScale = 0x1p-100f;
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -48,28 +59,28 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two bytes picked by `sel` (0x4140: bytes 0, 1; 0x4342: bytes 2, 3) as the
-// fp16 pair of byte - 128.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
-  const uint32_t m = __byte_perm(w, 0x64646464u, sel);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+// Bytes 0, 1 (2, 3) of a word as the fp16 pair of byte 2^-24.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return __byte_perm(w, 0u, 0x4140); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return __byte_perm(w, 0u, 0x4342); }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// The 8 x 8 fp16 matrix whose row lane / 4 holds columns 2 (lane % 4), + 1, transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ float tanh_fast(float x) {
+  float r;  // 1 - 2 / (1 + e^2x): within 2^-22 absolutely, which is what a score needs
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(2.f * kLog2e * x)));
+  return fmaf(-2.f, r, 1.f);
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -82,23 +93,49 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-template <int D, int RT>
+// D: the head's size rounded up to 64, 128 or 256. NR: query rows in eights.
+// A stage holds 16-token groups: K's boxes, then V's, each of 16 rows of 64 or
+// 128 bytes (two boxes side by side at D = 256), swizzled by the copy.
+template <int D, int NR>
 struct Shape {
-  static constexpr int kRows = 16 * RT;
-  static constexpr int kTile = D == 256 ? 16 : 32;  // tokens a stage
+  static constexpr int kRows = 8 * NR;
+  // Accumulators and queries take 3 D NR / 8 registers a thread: 16 warps an SM
+  // where that and 16 rings fit, else 8.
+  static constexpr int kWarps = D * NR <= 128 ? 16 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = 3;
+  static constexpr int kTile = D * kWarps <= 1024 ? 32 : 16;  // tokens a stage
   static constexpr int kGroups = kTile / 16;
-  static constexpr int kKBytes = kTile * D;
-  static constexpr int kStageBytes = 2 * kKBytes;
-  static constexpr int kScaleBytes = 16;  // (K, V) scale of each 16-token group
-  static constexpr int kWarpBytes = kStages * (kStageBytes + kScaleBytes);
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kPitch = D == 64 ? 64 : 128;
+  static constexpr int kBoxes = D / kPitch;
+  static constexpr int kBoxBytes = 16 * kPitch;
+  static constexpr int kGroupBytes = 2 * 16 * D;
+  static constexpr int kStageBytes = kGroups * kGroupBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kSmem = kWarps * kWarpBytes + 1024;  // the base is rounded up to 1024
+  static_assert(kSmem + 12288 <= 232448, "rings and the static arrays fit an SM");
+};
+
+// A warp's ring: its stages, their barriers and scales, and where it stands.
+template <int D, int NR>
+struct Ring {
+  using S = Shape<D, NR>;
+  uint32_t base;
+  uint64_t* full;   // kStages
+  float2* scales;   // kStages x kGroups: (K, V) scale; V < 0: nothing to see
+  const void* map_k;
+  const void* map_v;
+  uint64_t wait_ns;
+  int stage;
+  uint32_t parity;
 };
 
 // How an item's rows and tokens lie.
 struct RowTile {
   int i0;       // first query token of the tile
   int rows;     // rows of the tile (head-major within a token)
-  int j0, j1;   // tokens that some row sees, j0 rounded down to a tile
+  int lo;       // first token that some row sees
+  int j0, j1;   // lo rounded down to a tile, and the end of the tokens seen
   int tiles;    // at least 1
 };
 template <int ROWS, int TILE>
@@ -110,8 +147,8 @@ __device__ __forceinline__ RowTile row_tile(const AttendArgs& a, const Seq& s, i
   const int i1 = (first + t.rows - 1) / a.group;
   const int base = s.len - s.n;
   t.j1 = max(base + i1 + 1, 0);
-  t.j0 = a.window > 0 ? max(base + t.i0 - a.window + 1, 0) : 0;
-  t.j0 &= ~(TILE - 1);
+  t.lo = a.window > 0 ? max(base + t.i0 - a.window + 1, 0) : 0;
+  t.j0 = t.lo & ~(TILE - 1);
   t.tiles = max((t.j1 - t.j0 + TILE - 1) / TILE, 1);
   return t;
 }
@@ -120,367 +157,506 @@ __device__ __forceinline__ int row_tiles(const AttendArgs& a, const Seq& s) {
   return (s.n * a.group + ROWS - 1) / ROWS;
 }
 
-// Partial sums of one warp's piece of a shared item: per row the maximum
-// (base 2), the sum of exponentials, and the d unnormalised outputs.
+// Partial sums of a piece of a shared item: per row the d outputs before the
+// division, then (maximum, sum of exponentials), base 2.
 struct Scratch {
-  int64_t* prefix;  // n_seqs + 1: tiles before each sequence
-  float* parts;     // 2 slots a warp
-  int slot_floats;  // rows * (d + 2)
+  float* parts;   // 2 slots a warp: the piece its range starts with, the one it ends with
+  float* joined;  // 2 slots a CTA, the same over its warps
+  struct Open* open;  // a CTA each
+  int rows;       // rows a slot holds
+  int slot_floats;
+};
+// The item that a CTA's range ends within, if it starts in that CTA.
+struct Open {
+  int s, rt, h, any;
+  int64_t ts, te;
+  int64_t total, ctas;
 };
 
 __host__ __device__ __forceinline__ int part_rows(int max_new, int group, int rows) {
   return max_new * group < rows ? max_new * group : rows;
 }
+__host__ __device__ __forceinline__ int part_floats(int rows, int d) { return rows * d + (2 * rows + 3) / 4 * 4; }
 
-template <int D, int RT>
+// [first(i), first(i + 1)): part i of `total` cut into n parts as equal as can be.
+struct Cut {
+  int64_t each;
+  int rest;
+  __device__ __forceinline__ Cut(int64_t total, int n) {
+    if (total <= 0x7fffffff) {
+      each = static_cast<uint32_t>(total) / static_cast<uint32_t>(n);
+      rest = static_cast<uint32_t>(total) % static_cast<uint32_t>(n);
+    } else {
+      each = total / n;
+      rest = static_cast<int>(total % n);
+    }
+  }
+  __device__ __forceinline__ int64_t first(int i) const { return each * i + min(i, rest); }
+};
+
+// Where an item's row goes.
+struct RowOut {
+  int64_t row;
+  int head;
+};
+template <int ROWS>
+__device__ __forceinline__ RowOut row_out(const AttendArgs& a, const Seq& sq, int h, int rt, int lr) {
+  const int row = rt * ROWS + lr, qi = row / a.group;
+  return RowOut{int64_t(sq.r0) + qi, h * a.group + row - qi * a.group};
+}
+
+template <int D, int NR>
 struct Worker {
-  using S = Shape<D, RT>;
-  static constexpr int kNt = D / 8;       // n-tiles of the output
-  static constexpr int kJ = D / 64;       // 64-value steps of a key
-  static constexpr int kPitch = D;
+  using S = Shape<D, NR>;
+  static constexpr int kMt = D / 16;  // m-tiles of the output
+  static constexpr int kJ = D / 64;   // 64-value steps of a key
 
-  // One warp's pass over tiles [t0, t1) of an item.
-  static __device__ __forceinline__ void run(const AttendArgs& a, const Seq& sq, int s, int h, int rt, int t0, int t1,
-                                             bool whole, float* part, uint32_t ring) {
+  // One warp's pass over tiles [t0, t1) of an item. False: a wait gave up.
+  static __device__ __forceinline__ bool run(const AttendArgs& a, const Seq& sq, int s, int h, int rt, int t0, int t1,
+                                             bool whole, const Scratch& scr, int slot, Ring<D, NR>& ring) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const RowTile it = row_tile<S::kRows, S::kTile>(a, sq, rt);
     const int d = a.c.d, chunks = d >> 4;
     const int first_row = rt * S::kRows;
 
-    // ---- the queries in fragment order: value c of chunk 4 j + t, two MMAs' rows
-    uint32_t qf[RT][kJ * 4][4];
-    float fac[RT][2];
-    int place[RT][2];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int lr = 16 * r + 8 * e + g;
-        const bool ok = lr < it.rows;
-        const int row = first_row + lr, qi = row / a.group, hg = row - qi * a.group;
-        place[r][e] = ok ? sq.len - sq.n + qi : -1;
-        const uint16_t* qp = a.q + (sq.r0 + qi) * a.q_stride + int64_t(h * a.group + hg) * d;
-        uint4 raw[kJ][2];
-        float mx = 0.f;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const int c = 4 * j + t;
-          const bool in = ok && c < chunks;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            raw[j][k] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-          }
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int ex = __float_as_int(mx) >> 23;  // 2^(ex - 127) <= mx < 2^(ex - 126)
-        ex = ex < 1 || ex > 253 ? 127 : ex;
-        const float down = __int_as_float((254 - ex) << 23);
-        fac[r][e] = __int_as_float(ex << 23) * a.scale;
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // values 8 k + 2 i, + 1 of the chunk: MMA 4 j + 2 k + i / 2, half i % 2
-              qf[r][4 * j + 2 * k + i / 2][2 * (i & 1) + e] =
-                  f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-          }
-        }
-      }
-    }
-
-    float o[RT][kNt][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int i = 0; i < kNt; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
-    float m[RT][2], l[RT][2], vmax = 0.f;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) m[r][0] = m[r][1] = -INFINITY, l[r][0] = l[r][1] = 0.f;
-
-    // ---- the ring
+    // ---- the ring: lane i holds the page of index page0 + i and its scales, and starts its copies
     const int page = a.c.page, log2p = a.c.page_log2;
-    int pid_first = -1, pid_mine = -1;  // lane i: the page of index pid_first + i
+    int page0 = -32, pid = -1;
+    float2 mine = make_float2(0.f, -1.f);
     auto issue = [&](int tile, int stage) {
-      const uint32_t kb = ring + stage * (S::kStageBytes + S::kScaleBytes), vb = kb + S::kKBytes;
-      const uint32_t sb = kb + S::kStageBytes;
 #pragma unroll
       for (int gi = 0; gi < S::kGroups; ++gi) {
         const int j = it.j0 + tile * S::kTile + gi * 16;
-        if (j < it.j1) {  // warp-uniform
+        uint64_t* bar = ring.full + stage;
+        float2* sc = ring.scales + stage * S::kGroups + gi;
+        if (j < it.j1 && j + 16 > it.lo) {  // warp-uniform
           const int index = j >> log2p;
-          if (pid_first < 0 || index >= pid_first + 32) {
-            pid_first = index;
-            pid_mine = (index + lane) << log2p < it.j1 ? load_page(a.c, a.b, s, index + lane, a.err) : -1;
-          }
-          const int pid = __shfl_sync(0xffffffffu, pid_mine, index - pid_first);
-          if (pid >= 0) {
-            const int64_t tl = int64_t(pid) * a.c.heads + h;
-            if (lane == 0) cp_async_4_at(sb + gi * 8, a.c.k_scale + tl);
-            if (lane == 1) cp_async_4_at(sb + gi * 8 + 4, a.c.v_scale + tl);
-            const int64_t off = (tl * page + (j & (page - 1))) * d;
-            constexpr int kPerRow = D / 16;           // chunks of a padded row
-            constexpr int kRowsPer = 32 / kPerRow;    // rows one instruction covers
-            const int c = lane % kPerRow, r0 = lane / kPerRow;
-            if (c < chunks) {
-#pragma unroll
-              for (int r = 0; r < 16; r += kRowsPer) {
-                const int row = gi * 16 + r + r0;
-                const uint32_t sm = row * kPitch + (swz(row, c) << 4);
-                const int64_t go = off + int64_t(r + r0) * d + c * 16;
-                cp_async_16(kb + sm, a.c.k + go);
-                cp_async_16(vb + sm, a.c.v + go);
-              }
+          if (index >= page0 + 32) {
+            page0 = index;
+            pid = index + lane <= (it.j1 - 1) >> log2p ? load_page(a.c, a.b, s, index + lane, a.err) : -1;
+            mine = make_float2(0.f, -1.f);
+            if (pid >= 0) {
+              const int64_t at = int64_t(pid) * a.c.heads + h;
+              mine = make_float2(__ldg(a.c.k_scale + at), __ldg(a.c.v_scale + at));
             }
-            continue;
+          }
+          if (lane == index - page0) {
+            *sc = mine;
+            if (pid >= 0) {
+              const uint32_t kb = ring.base + stage * S::kStageBytes + gi * S::kGroupBytes, vb = kb + 16 * D;
+              const int row = h * page + (j & (page - 1));
+              mbar_arrive_expect_tx(bar, S::kGroupBytes);
+#pragma unroll
+              for (int x = 0; x < S::kBoxes; ++x) {
+                tma_load_3d(kb + x * S::kBoxBytes, ring.map_k, 128 * x, row, pid, bar);
+                tma_load_3d(vb + x * S::kBoxBytes, ring.map_v, 128 * x, row, pid, bar);
+              }
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+        } else if (lane == 0) {
+          *sc = make_float2(0.f, -1.f);
+          mbar_arrive(bar);
+        }
+      }
+    };
+    const int stage0 = ring.stage;
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) {
+      int st = stage0 + i;
+      if (st >= S::kStages) st -= S::kStages;
+      if (t0 + i < t1) issue(t0 + i, st);
+    }
+
+    // ---- the queries in fragment order: lane (g, t) holds chunks 4 j + t of row g. The codes
+    // enter the products as byte 2^-24 (an fp16 subnormal, exact); the sums start at
+    // -128 2^-24 times the query's own sum.
+    uint32_t qf[NR][kJ * 4][2];
+    float fac[NR][2], bias[NR][2];   // of rows 2 t, 2 t + 1
+    int place[NR][2];
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int lr = 8 * r + g;
+      const bool ok = lr < it.rows;
+      const int row = first_row + lr, qi = row / a.group, hg = row - qi * a.group;
+      const uint16_t* qp = a.q + (sq.r0 + qi) * a.q_stride + int64_t(h * a.group + hg) * d;
+      uint4 raw[kJ][2];
+      float mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int c = 4 * j + t;
+        const bool in = ok && c < chunks;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          raw[j][k] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int ex = __float_as_int(mx) >> 23;  // 2^(ex - 127) <= mx < 2^(ex - 126)
+      ex = ex < 1 || ex > 253 ? 127 : ex;
+      const float down = __int_as_float((254 - ex) << 23) * sign;
+      const float up = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
+      const int pl = ok ? sq.len - sq.n + qi : -1;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // values 8 k + 2 i, + 1 of the chunk: product 4 j + 2 k + i / 2, half i % 2
+            const uint32_t h2 = f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
+            qf[r][4 * j + 2 * k + i / 2][i & 1] = h2;
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            sum += f.x + f.y;
           }
         }
-        if (lane == 0) {  // nothing to see: a negative V scale masks the group
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(sb + gi * 8), "f"(0.f), "f"(-1.f) : "memory");
-        }
       }
-      cp_async_commit();
-    };
-
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (t0 + i < t1) issue(t0 + i, i);
-      else cp_async_commit();
-    }
-    int stage = 0;
-    for (int tile = t0; tile < t1; ++tile) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      {
-        int ahead = stage + kStages - 1;
-        if (ahead >= kStages) ahead -= kStages;
-        if (tile + kStages - 1 < t1) issue(tile + kStages - 1, ahead);
-        else cp_async_commit();
+      for (int e = 0; e < 2; ++e) {
+        fac[r][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
+        bias[r][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e)) * (-128.f * kCode);
+        place[r][e] = __shfl_sync(0xffffffffu, pl, 4 * (2 * t + e));
       }
-      const uint32_t kb = ring + stage * (S::kStageBytes + S::kScaleBytes), vb = kb + S::kKBytes;
-      const uint32_t sb = kb + S::kStageBytes;
-      if (++stage == kStages) stage = 0;
+    }
+
+    float o[NR][kMt][4], ps[NR][4];  // ps: 128 2^-24 times the probabilities' sum
+    float m[NR][2], l[NR][2], vmax = kTinyScale, vinv = kPScale / kTinyScale;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r][0] = l[r][1] = 0.f;
+      ps[r][0] = ps[r][1] = ps[r][2] = ps[r][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMt; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
+    }
+    // the places of the tile's first and last query token
+    const int lo_place = sq.len - sq.n + it.i0;
+    const int hi_place = sq.len - sq.n + (first_row + it.rows - 1) / a.group;
+    const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    // where this lane's chunks lie in a box: K rows g ^ ((g & 1) << 2) and + 8, V rows 2 t, (2 t + 1) ^ 4 and + 8
+    const int krow = g ^ ((g & 1) << 2), va_row = 2 * t, vb_row = (2 * t + 1) ^ 4;
+
+    for (int tile = t0; tile < t1; ++tile) {
+      const int stage = ring.stage;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(ring.full + stage, ring.parity, ring.wait_ns))) {
+        if (lane == 0) atomicOr(a.err, kErrWaitFull);
+        // the copies in flight: this tile's and the next's
+        for (int i = 0; i < S::kStages - 1 && tile + i < t1; ++i) {
+          if (!mbar_wait_bounded(ring.full + ring.stage, ring.parity, 1000000000ull) && lane == 0) atomicOr(a.err, kErrDrain);
+          if (++ring.stage == S::kStages) ring.stage = 0, ring.parity ^= 1;
+        }
+        return false;
+      }
+      {
+        int ahead = stage + S::kStages - 1;
+        if (ahead >= S::kStages) ahead -= S::kStages;
+        if (tile + S::kStages - 1 < t1) issue(tile + S::kStages - 1, ahead);
+      }
+      if (++ring.stage == S::kStages) ring.stage = 0, ring.parity ^= 1;
+      const uint32_t sb = ring.base + stage * S::kStageBytes;
       float ks[S::kGroups], vs[S::kGroups];
       bool dead = false;
-#pragma unroll
-      for (int gi = 0; gi < S::kGroups; ++gi) {
-        const uint2 sc = lds64(sb + gi * 8);
-        ks[gi] = __uint_as_float(sc.x);
-        vs[gi] = __uint_as_float(sc.y);
-        dead |= vs[gi] < 0.f;
-      }
-      // ---- scores
-      float sc[RT][S::kGroups * 2][4];
-#pragma unroll
-      for (int nt = 0; nt < S::kGroups * 2; ++nt) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) sc[r][nt][0] = sc[r][nt][1] = sc[r][nt][2] = sc[r][nt][3] = 0.f;
-        const int row = nt * 8 + (g ^ ((g & 1) << 2));
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-          const uint4 w = lds128(kb + row * kPitch + (swz(row, 4 * j + t) << 4));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t b0 = codes_f16(ww[i], 0x4140), b1 = codes_f16(ww[i], 0x4342);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              const uint32_t(&q)[4] = qf[r][4 * j + i];
-              mma_f16_16816(sc[r][nt], q[0], q[1], q[2], q[3], b0, b1);
-            }
-          }
-        }
-      }
-      // ---- scale, cap, mask (base 2 from here)
-      const int jt = it.j0 + tile * S::kTile;
-      // every token of the tile is seen by every row?
-      const int lo_place = sq.len - sq.n + it.i0;
-      const int hi_place = sq.len - sq.n + (first_row + it.rows - 1) / a.group;
-      const bool masked = dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-#pragma unroll
-        for (int nt = 0; nt < S::kGroups * 2; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = fac[r][e >> 1] * ks[nt >> 1];
-            float x = sc[r][nt][e];
-            if (a.softcap > 0.f) {
-              x = a.softcap * kLog2e * tanhf(x * f / a.softcap);
-            } else {
-              x *= f * kLog2e;
-            }
-            if (masked) {
-              const int j = jt + nt * 8 + ((e & 1) ? ((2 * t + 1) ^ 4) : 2 * t);
-              const int p = place[r][e >> 1];
-              if (j > p || (a.window > 0 && j <= p - a.window) || vs[nt >> 1] < 0.f) x = -INFINITY;
-            }
-            sc[r][nt][e] = x;
-          }
-        }
-      }
-      // ---- running maxima; the outputs are rescaled only when one grew
       float vnew = vmax;
 #pragma unroll
-      for (int gi = 0; gi < S::kGroups; ++gi) vnew = fmaxf(vnew, vs[gi]);
-      float mn[RT][2];
+      for (int gi = 0; gi < S::kGroups; ++gi) {
+        const float2 f = ring.scales[stage * S::kGroups + gi];
+        ks[gi] = f.x;
+        vs[gi] = f.y;
+        dead |= f.y < 0.f;
+        vnew = fmaxf(vnew, f.y);
+      }
+      // ---- scores: element e of sc[r][gi] is token slot g + 8 (e / 2), row 2 t + e % 2
+      float sc[NR][S::kGroups][4], f[NR][S::kGroups][2];
+#pragma unroll
+      for (int gi = 0; gi < S::kGroups; ++gi) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[r][gi][e] = bias[r][e & 1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) f[r][gi][e] = fac[r][e] * ks[gi];
+        }
+        const uint32_t kb = sb + gi * S::kGroupBytes;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const uint4 x = lds128(kb + at(krow, 4 * j + t)), y = lds128(kb + at(krow + 8, 4 * j + t));
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = codes_lo(xw[i]), a1 = codes_lo(yw[i]), a2 = codes_hi(xw[i]), a3 = codes_hi(yw[i]);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) mma_f16_16816(sc[r][gi], a0, a1, a2, a3, qf[r][4 * j + i][0], qf[r][4 * j + i][1]);
+          }
+        }
+      }
+      // ---- cap and mask, where there is one; a score (base 2) is then sc f
+      const int jt = it.j0 + tile * S::kTile;
+      const bool masked = dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int gi = 0; gi < S::kGroups; ++gi)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) f[r][gi][e] *= 1.f / kCode;
+      if (masked || a.softcap > 0.f) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int gi = 0; gi < S::kGroups; ++gi) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = sc[r][gi][e] * f[r][gi][e & 1];
+              if (a.softcap > 0.f) x = cap_out * tanh_fast(x * cap_in);
+              const int j = jt + gi * 16 + krow + 8 * (e >> 1), p = place[r][e & 1];
+              if (j > p || (a.window > 0 && j <= p - a.window) || vs[gi] < 0.f) x = -INFINITY;
+              sc[r][gi][e] = x;
+            }
+            f[r][gi][0] = f[r][gi][1] = 1.f;
+          }
+        }
+      }
+      // ---- raise the running maxima where a score passes one by the slack
+      float top[NR][2];
       bool grew = vnew > vmax;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int r = 0; r < NR; ++r) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = m[r][e];
+          float x = fmaxf(sc[r][0][e], sc[r][0][2 + e]) * f[r][0][e];
 #pragma unroll
-          for (int nt = 0; nt < S::kGroups * 2; ++nt) x = fmaxf(x, fmaxf(sc[r][nt][2 * e], sc[r][nt][2 * e + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          mn[r][e] = x;
-          grew |= x > m[r][e];
+          for (int gi = 1; gi < S::kGroups; ++gi) x = fmaxf(x, fmaxf(sc[r][gi][e], sc[r][gi][2 + e]) * f[r][gi][e]);
+          top[r][e] = x;
+          grew |= x > m[r][e] + kSlack;
         }
       }
       if (__any_sync(0xffffffffu, grew)) {
-        const float vr = vmax > 0.f ? vmax / vnew : 0.f;
+        const float vr = vmax / vnew;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
+        for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float k = mn[r][e] == -INFINITY ? 1.f : exp2_fast(m[r][e] - mn[r][e]);
-            l[r][e] *= k;
-            m[r][e] = mn[r][e];
+            float x = fmaxf(top[r][e], m[r][e]);
 #pragma unroll
-            for (int i = 0; i < kNt; ++i) o[r][i][2 * e] *= k * vr, o[r][i][2 * e + 1] *= k * vr;
+            for (int sh = 4; sh < 32; sh <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sh));
+            const float k = x == -INFINITY ? 1.f : exp2_fast(m[r][e] - x);
+            l[r][e] *= k;
+            m[r][e] = x;
+            const float kv = k * vr;
+            ps[r][e] *= kv, ps[r][2 + e] *= kv;
+#pragma unroll
+            for (int i = 0; i < kMt; ++i) o[r][i][e] *= kv, o[r][i][2 + e] *= kv;
           }
         }
         vmax = vnew;
+        vinv = kPScale / vnew;
       }
       // ---- probabilities and outputs
-      float ratio[S::kGroups];
-#pragma unroll
-      for (int gi = 0; gi < S::kGroups; ++gi) ratio[gi] = vs[gi] > 0.f ? vs[gi] / vmax * kPScale : 0.f;
 #pragma unroll
       for (int gi = 0; gi < S::kGroups; ++gi) {
-        uint32_t pf[RT][4];
+        const float ratio = fmaxf(vs[gi], 0.f) * vinv;
+        uint32_t pf[NR][2];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float top = m[r][e] == -INFINITY ? 0.f : m[r][e];
-            float p[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = exp2_fast(sc[r][2 * gi + (k >> 1)][2 * e + (k & 1)] - top);
-            l[r][e] += (p[0] + p[1]) + (p[2] + p[3]);
-            pf[r][e] = f16x2(p[0] * ratio[gi], p[1] * ratio[gi]);
-            pf[r][2 + e] = f16x2(p[2] * ratio[gi], p[3] * ratio[gi]);
-          }
+        for (int r = 0; r < NR; ++r) {
+          const float m0 = m[r][0] == -INFINITY ? 0.f : m[r][0], m1 = m[r][1] == -INFINITY ? 0.f : m[r][1];
+          const float p0 = exp2_fast(fmaf(sc[r][gi][0], f[r][gi][0], -m0)), p1 = exp2_fast(fmaf(sc[r][gi][1], f[r][gi][1], -m1));
+          const float p2 = exp2_fast(fmaf(sc[r][gi][2], f[r][gi][0], -m0)), p3 = exp2_fast(fmaf(sc[r][gi][3], f[r][gi][1], -m1));
+          l[r][0] += p0 + p2;
+          l[r][1] += p1 + p3;
+          pf[r][0] = transpose_8x8(f16x2(p0 * ratio, p1 * ratio));
+          pf[r][1] = transpose_8x8(f16x2(p2 * ratio, p3 * ratio));
+          mma_f16_16816(ps[r], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, pf[r][0], pf[r][1]);
         }
-        const int ra = gi * 16 + 2 * t, rb = gi * 16 + ((2 * t + 1) ^ 4);
-        auto columns = [&](const uint32_t va, const uint32_t vbw, const uint32_t vc, const uint32_t vd, int nt) {
-          // four n-tiles: byte i of the words is the column of n-tile nt + i
+        const uint32_t vb = sb + gi * S::kGroupBytes + 16 * D;
+        // four bytes of four tokens: two m-tiles, values 2 i of their run on rows g, 2 i + 1 on rows g + 8
+        auto columns = [&](const uint32_t va, const uint32_t vbw, const uint32_t vc, const uint32_t vd, int mt) {
           const uint32_t x0 = __byte_perm(va, vbw, 0x5140), x1 = __byte_perm(va, vbw, 0x7362);
           const uint32_t y0 = __byte_perm(vc, vd, 0x5140), y1 = __byte_perm(vc, vd, 0x7362);
-          const uint32_t b0[4] = {codes_f16(x0, 0x4140), codes_f16(x0, 0x4342), codes_f16(x1, 0x4140), codes_f16(x1, 0x4342)};
-          const uint32_t b1[4] = {codes_f16(y0, 0x4140), codes_f16(y0, 0x4342), codes_f16(y1, 0x4140), codes_f16(y1, 0x4342)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int r = 0; r < NR; ++r)
+            mma_f16_16816(o[r][mt], codes_lo(x0), codes_hi(x0), codes_lo(y0), codes_hi(y0), pf[r][0], pf[r][1]);
 #pragma unroll
-            for (int r = 0; r < RT; ++r) mma_f16_16816(o[r][nt + i], pf[r][0], pf[r][1], pf[r][2], pf[r][3], b0[i], b1[i]);
+          for (int r = 0; r < NR; ++r)
+            mma_f16_16816(o[r][mt + 1], codes_lo(x1), codes_hi(x1), codes_lo(y1), codes_hi(y1), pf[r][0], pf[r][1]);
         };
         if constexpr (D == 64) {
-          auto at = [&](int row) { return lds64(vb + row * kPitch + (swz(row, g >> 1) << 4) + (g & 1) * 8); };
-          const uint2 va = at(ra), vbw = at(rb), vc = at(ra + 8), vd = at(rb + 8);
+          auto get = [&](int row) { return lds64(vb + at(row, g >> 1) + (g & 1) * 8); };
+          const uint2 va = get(va_row), vbw = get(vb_row), vc = get(va_row + 8), vd = get(vb_row + 8);
           columns(va.x, vbw.x, vc.x, vd.x, 0);
-          columns(va.y, vbw.y, vc.y, vd.y, 4);
+          columns(va.y, vbw.y, vc.y, vd.y, 2);
         } else {
 #pragma unroll
           for (int hi = 0; hi < D / 128; ++hi) {
-            auto at = [&](int row) { return lds128(vb + row * kPitch + (swz(row, g + 8 * hi) << 4)); };
-            const uint4 va = at(ra), vbw = at(rb), vc = at(ra + 8), vd = at(rb + 8);
-            columns(va.x, vbw.x, vc.x, vd.x, 16 * hi);
-            columns(va.y, vbw.y, vc.y, vd.y, 16 * hi + 4);
-            columns(va.z, vbw.z, vc.z, vd.z, 16 * hi + 8);
-            columns(va.w, vbw.w, vc.w, vd.w, 16 * hi + 12);
+            auto get = [&](int row) { return lds128(vb + at(row, g + 8 * hi)); };
+            const uint4 va = get(va_row), vbw = get(vb_row), vc = get(va_row + 8), vd = get(vb_row + 8);
+            columns(va.x, vbw.x, vc.x, vd.x, 8 * hi);
+            columns(va.y, vbw.y, vc.y, vd.y, 8 * hi + 2);
+            columns(va.z, vbw.z, vc.z, vd.z, 8 * hi + 4);
+            columns(va.w, vbw.w, vc.w, vd.w, 8 * hi + 6);
           }
         }
       }
       __syncwarp();  // the stage is read before it is filled again
     }
-    cp_async_wait<0>();
-    __syncwarp();
 
-    // ---- out: column of o[r][nt][2 e + x] is kRun (2 t + x) + nt % kRun + 128 (nt / 16)
+    // ---- out: row 2 t + e of eight r, values kRun g + 2 i (o[.][i][e]) and + 1 (o[.][i][2 + e]), in runs of kRun
     constexpr int kRun = D == 64 ? 8 : 16;
+    constexpr float kBack = 1.f / (kCode * kPScale);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+    for (int r = 0; r < NR; ++r) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 1);
-        l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], 2);
-        const int lr = 16 * r + 8 * e + g;
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], sh);
+        const int lr = 8 * r + 2 * t + e;
         if (lr >= it.rows) continue;
+        auto value = [&](int i, int half) { return (o[r][i][2 * half + e] - ps[r][e]) * kBack; };
         if (!whole) {
-          float* p = part + int64_t(lr) * (d + 2);
-          const float back = vmax * (1.f / kPScale);
-          if (t == 0) p[d] = m[r][e], p[d + 1] = l[r][e];
+          float* p = scr.parts + int64_t(slot) * scr.slot_floats;
+          if (g == 0) *reinterpret_cast<float2*>(p + scr.rows * d + 2 * lr) = make_float2(m[r][e], l[r][e]);
+          p += lr * d;
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int nt = 0; nt < kNt; nt += 2) {
-              const int col = kRun * (2 * t + x) + nt % kRun + 128 * (nt / 16);
-              if (col < d)
-                *reinterpret_cast<float2*>(p + col) = make_float2(o[r][nt][2 * e + x] * back, o[r][nt + 1][2 * e + x] * back);
-            }
+          for (int i = 0; i < kMt; i += 2) {
+            const int col = kRun * g + 2 * (i % 8) + 128 * (i / 8);
+            if (col < d)
+              *reinterpret_cast<float4*>(p + col) = make_float4(value(i, 0) * vmax, value(i, 1) * vmax, value(i + 1, 0) * vmax,
+                                                                value(i + 1, 1) * vmax);
+          }
           continue;
         }
-        const int row = first_row + lr, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-        const int64_t grow = sq.r0 + qi;
-        const float inv = l[r][e] > 0.f ? vmax * (1.f / kPScale) / l[r][e] : (l[r][e] == 0.f ? 0.f : l[r][e]);
-        if (a.lse && t == 0)
-          a.lse[grow * (a.c.heads * a.group) + hq] = l[r][e] == 0.f ? -INFINITY : (m[r][e] + log2f(l[r][e])) * kLn2;
-        uint16_t* op = a.out + grow * a.out_stride + int64_t(hq) * d;
+        const RowOut ro = row_out<S::kRows>(a, sq, h, rt, lr);
+        const float inv = l[r][e] > 0.f ? vmax / l[r][e] : (l[r][e] == 0.f ? 0.f : l[r][e]);
+        if (a.lse && g == 0)
+          a.lse[ro.row * (a.c.heads * a.group) + ro.head] = l[r][e] == 0.f ? -INFINITY : (m[r][e] + log2f(l[r][e])) * kLn2;
+        uint16_t* op = a.out + ro.row * a.out_stride + int64_t(ro.head) * d;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int i = 0; i < kMt; i += 4) {
+          const int col = kRun * g + 2 * (i % 8) + 128 * (i / 8);
+          if (col < d) {
+            uint32_t w[4];
 #pragma unroll
-          for (int nt = 0; nt < kNt; nt += 8) {
-            const int col = kRun * (2 * t + x) + nt % kRun + 128 * (nt / 16);
-            if (col < d) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(o[r][nt + 2 * i][2 * e + x] * inv, o[r][nt + 2 * i + 1][2 * e + x] * inv);
-                w[i] = *reinterpret_cast<const uint32_t*>(&b);
-              }
-              *reinterpret_cast<uint4*>(op + col) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(value(i + k, 0) * inv, value(i + k, 1) * inv);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b);
             }
+            *reinterpret_cast<uint4*>(op + col) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+        }
       }
     }
+    return true;
   }
 
-  // Where 16-byte chunk c of a stage's row lies: 8 rows' chunks spread so that
-  // both the score reads (rows g ^ ((g & 1) << 2), chunks 4 j + t) and the value
-  // reads (rows 2 t, chunk g) meet no bank twice (64-byte rows: twice).
-  static __device__ __forceinline__ int swz(int row, int c) {
-    if constexpr (D == 64) return c ^ ((row >> 1) & 3);
-    else return c ^ (row & 7);
-  }
-  static __device__ __forceinline__ void cp_async_4_at(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+  // Where 16-byte chunk c of a group's row lies, as the copy swizzles it: the
+  // score reads (rows krow, chunks 4 j + t) and the value reads (rows 2 t,
+  // chunk g) then meet no bank twice (64-byte rows: twice).
+  static __device__ __forceinline__ uint32_t at(int row, int c) {
+    if constexpr (D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    else return (c >> 3) * S::kBoxBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4);
   }
 };
 
+// Joins one row of n pieces (piece i in slot slot_of(i)), in their order, by one
+// warp: the pieces' weights first, a lane each, then the sums.
+template <int D>
+struct Joined {
+  static constexpr int kCols = D / 32;
+  float o[kCols], m, l;
+};
+template <int D, typename SlotOf>
+__device__ __forceinline__ void join_row(const float* parts, int slot_floats, int rows, int d, int lr, int n, SlotOf slot_of,
+                                         Joined<D>& r) {
+  constexpr int kCols = Joined<D>::kCols, kVec = kCols < 4 ? kCols : 4;
+  const int lane = threadIdx.x & 31;
+  r.m = -INFINITY;
+  r.l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) r.o[i] = 0.f;
+  for (int first = 0; first < n; first += 32) {
+    const bool have = first + lane < n;
+    const int64_t mine = have ? int64_t(slot_of(first + lane)) * slot_floats : 0;
+    const float2 ml = have ? __ldcg(reinterpret_cast<const float2*>(parts + mine + rows * d + 2 * lr)) : make_float2(-INFINITY, 0.f);
+    float top = fmaxf(r.m, ml.x);
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+    const float to = top == -INFINITY ? 0.f : top;  // a NaN sum has no maximum and is passed on
+    const float keep = exp2_fast(r.m - to), weight = exp2_fast(ml.x - to);
+    float sum = ml.y * weight;
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+    r.l = r.l * keep + sum;
+    r.m = top;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) r.o[i] *= keep;
+    const int count = min(32, n - first);
+    constexpr int kBatch = D == 256 ? 4 : 8;
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      float v[kBatch][kCols], wt[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const bool ok = k0 + k < count;
+        const float* p = parts + __shfl_sync(0xffffffffu, mine, (k0 + k) & 31) + lr * d;
+        const float w = __shfl_sync(0xffffffffu, weight, (k0 + k) & 31);
+        wt[k] = ok ? w : 0.f;
+#pragma unroll
+        for (int i = 0; i < kCols; i += kVec) {
+          const int col = lane * kVec + 32 * i;
+          const bool in = ok && col < d;
+          if constexpr (kVec == 4) {
+            const float4 x = in ? __ldcg(reinterpret_cast<const float4*>(p + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[k][i] = x.x, v[k][i + 1] = x.y, v[k][i + 2] = x.z, v[k][i + 3] = x.w;
+          } else {
+            const float2 x = in ? __ldcg(reinterpret_cast<const float2*>(p + col)) : make_float2(0.f, 0.f);
+            v[k][i] = x.x, v[k][i + 1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(wt[k], v[k][i], r.o[i]);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void write_row(const AttendArgs& a, const RowOut& ro, const Joined<D>& r) {
+  constexpr int kCols = Joined<D>::kCols, kVec = kCols < 4 ? kCols : 4;
+  const int lane = threadIdx.x & 31, d = a.c.d;
+  const float inv = r.l > 0.f ? 1.f / r.l : (r.l == 0.f ? 0.f : r.l);
+  uint16_t* op = a.out + ro.row * a.out_stride + int64_t(ro.head) * d;
+#pragma unroll
+  for (int i = 0; i < kCols; i += kVec) {
+    const int col = lane * kVec + 32 * i;
+    if (col < d) {
+#pragma unroll
+      for (int k = 0; k < kVec; k += 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(r.o[i + k] * inv, r.o[i + k + 1] * inv);
+        *reinterpret_cast<__nv_bfloat162*>(op + col + k) = b;
+      }
+    }
+  }
+  if (a.lse && lane == 0) {
+    const float top = r.m == -INFINITY ? 0.f : r.m;
+    a.lse[ro.row * (a.c.heads * a.group) + ro.head] = r.l == 0.f ? -INFINITY : (top + log2f(r.l)) * kLn2;
+  }
+}
+
 // Tiles of a sequence in this kernel: none for one with more rows than `limit`
 // (the prompt kernel's).
-template <int D, int RT>
+template <int D, int NR>
 __device__ __forceinline__ int64_t seq_tiles(const AttendArgs& a, const Seq& s, int limit) {
-  using S = Shape<D, RT>;
+  using S = Shape<D, NR>;
   if (s.n * a.group > limit) return 0;
   int64_t t = 0;
   const int nrt = row_tiles<S::kRows>(a, s);
@@ -488,23 +664,33 @@ __device__ __forceinline__ int64_t seq_tiles(const AttendArgs& a, const Seq& s, 
   return t * a.c.heads;
 }
 
-constexpr int kThreads = kWarps * 32;
-
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, 1)
-kv_attend_kernel(const AttendArgs a, Scratch sc, int limit) {
-  using S = Shape<D, RT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+template <int D, int NR>
+__global__ void __launch_bounds__(Shape<D, NR>::kThreads, 1)
+kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const Scratch sc, int limit, uint64_t wait_ns) {
+  using S = Shape<D, NR>;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps;
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_pre[kThreads + 1];
   __shared__ int64_t s_warp[kWarps];
+  __shared__ uint64_t s_full[kWarps][S::kStages];
+  __shared__ float2 s_scales[kWarps][S::kStages * S::kGroups];
+  struct Piece {  // an unfinished piece of a warp
+    int64_t ts, te, begin;  // its item's tiles, and where the piece begins
+    int s, rt, h, any;
+  };
+  __shared__ Piece s_piece[2 * kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < kWarps * S::kStages) mbar_init(&s_full[0][0] + tid, S::kGroups);
+  if (tid < 2 * kWarps) s_piece[tid].any = 0;
+  fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // ---- tiles before each run of sequences
   const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
   int64_t mine = 0;
   for (int i = tid * per; i < min((tid + 1) * per, a.b.n_seqs); ++i)
-    mine += seq_tiles<D, RT>(a, load_seq(a.b, i, blockIdx.x == 0 ? a.err : nullptr), limit);
+    mine += seq_tiles<D, NR>(a, load_seq(a.b, i, blockIdx.x == 0 ? a.err : nullptr), limit);
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -519,130 +705,131 @@ kv_attend_kernel(const AttendArgs a, Scratch sc, int limit) {
   if (tid == 0) s_pre[0] = 0;
   __syncthreads();
   const int64_t total = s_pre[kThreads];
-  if (blockIdx.x == 0) {  // for the joining kernel
-    int64_t at = s_pre[tid];
-    for (int i = tid * per; i < min((tid + 1) * per, a.b.n_seqs); ++i) {
-      sc.prefix[i] = at;
-      at += seq_tiles<D, RT>(a, load_seq(a.b, i, nullptr), limit);
-    }
-    if (tid == 0) sc.prefix[a.b.n_seqs] = total;
-  }
-  // ---- this warp's range
-  const int64_t nw = int64_t(gridDim.x) * kWarps;
-  const int64_t w = int64_t(blockIdx.x) * kWarps + warp;
-  int64_t at = w * total / nw;
-  const int64_t end = (w + 1) * total / nw;
-  if (at >= end) return;
-  int run = 0;
+  // ---- this CTA's range (a tile a warp at least), and this warp's
+  const int cta = blockIdx.x;
+  const int ctas = static_cast<int>(min(int64_t(gridDim.x), max((total + kWarps - 1) / kWarps, int64_t(1))));
+  if (tid == 0) sc.open[cta].any = 0;
+  if (cta >= ctas || total == 0) return;
+  const Cut cut_ctas(total, ctas);
+  const int64_t A = cut_ctas.first(cta), B = cut_ctas.first(cta + 1);
+  const Cut cut(B - A, kWarps);
+  int64_t at = A + cut.first(warp);
+  const int64_t end = A + cut.first(warp + 1);
+  if (at < end) {
+    int run = 0;
 #pragma unroll
-  for (int step = kThreads / 2; step > 0; step >>= 1)
-    if (s_pre[run + step] <= at) run += step;
-  int s = run * per;
-  int64_t off = at - s_pre[run];
-  Seq sq = load_seq(a.b, s, nullptr);
-  int64_t in_seq = seq_tiles<D, RT>(a, sq, limit);
-  const uint32_t ring = smem_u32(smem) + warp * S::kWarpBytes;
-  const int64_t range_start = at;
-  while (at < end) {
-    while (off >= in_seq) {  // the next sequence that has tiles
-      off -= in_seq;
-      ++s;
-      sq = load_seq(a.b, s, nullptr);
-      in_seq = seq_tiles<D, RT>(a, sq, limit);
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (s_pre[run + step] <= at) run += step;
+    int s = run * per;
+    int64_t off = at - s_pre[run];
+    Seq sq = load_seq(a.b, s, nullptr);
+    int64_t in_seq = seq_tiles<D, NR>(a, sq, limit);
+    Ring<D, NR> ring;
+    ring.base = ((smem_u32(smem) + 1023u) & ~1023u) + warp * S::kWarpBytes;
+    ring.full = s_full[warp];
+    ring.scales = s_scales[warp];
+    ring.map_k = &map_k;
+    ring.map_v = &map_v;
+    ring.wait_ns = wait_ns;
+    ring.stage = 0;
+    ring.parity = 0;
+    const int64_t begin = at;
+    while (at < end) {
+      while (off >= in_seq) {  // the next sequence that has tiles
+        off -= in_seq;
+        ++s;
+        sq = load_seq(a.b, s, nullptr);
+        in_seq = seq_tiles<D, NR>(a, sq, limit);
+      }
+      int rt = 0;
+      int64_t rest = off;
+      RowTile it = row_tile<S::kRows, S::kTile>(a, sq, 0);
+      while (rest >= int64_t(it.tiles) * a.c.heads) {
+        rest -= int64_t(it.tiles) * a.c.heads;
+        it = row_tile<S::kRows, S::kTile>(a, sq, ++rt);
+      }
+      const int h = static_cast<int>(rest / it.tiles), t0 = static_cast<int>(rest % it.tiles);
+      const int t1 = static_cast<int>(min(int64_t(it.tiles), t0 + (end - at)));
+      const bool whole = t0 == 0 && t1 == it.tiles;
+      const int slot = 2 * warp + (at == begin ? 0 : 1);
+      if (!whole && lane == 0) s_piece[slot] = Piece{at - t0, at - t0 + it.tiles, at, s, rt, h, 1};
+      if (!Worker<D, NR>::run(a, sq, s, h, rt, t0, t1, whole, sc, 2 * kWarps * cta + slot, ring)) break;
+      at += t1 - t0;
+      off += t1 - t0;
     }
-    int rt = 0;
-    int64_t rest = off;
-    RowTile it = row_tile<S::kRows, S::kTile>(a, sq, 0);
-    while (rest >= int64_t(it.tiles) * a.c.heads) {
-      rest -= int64_t(it.tiles) * a.c.heads;
-      it = row_tile<S::kRows, S::kTile>(a, sq, ++rt);
+  }
+  // ---- pieces of one item in this CTA become one, or the item's outputs
+  __syncthreads();
+  int task = 0;
+  for (int i = 0; i < 2 * kWarps; ++i) {
+    const Piece p = s_piece[i];
+    if (!p.any || p.begin != max(p.ts, A)) continue;  // the first of its item here
+    const int w = i >> 1;
+    int n = 1;  // the others: what the next warps' ranges start with
+    while (w + n < kWarps && A + cut.first(w + n) < min(p.te, B)) ++n;
+    const Seq sq = load_seq(a.b, p.s, nullptr);
+    const int rows = row_tile<S::kRows, S::kTile>(a, sq, p.rt).rows;
+    const bool done = p.ts >= A && p.te <= B;
+    const int64_t to = int64_t(2 * cta + (p.ts < A ? 0 : 1)) * sc.slot_floats;
+    if (p.ts >= A && p.te > B && tid == 0) sc.open[cta] = Open{p.s, p.rt, p.h, 1, p.ts, p.te, total, ctas};
+    for (int lr = 0; lr < rows; ++lr) {
+      if (task++ % kWarps != warp) continue;
+      Joined<D> r;
+      join_row<D>(sc.parts + int64_t(2 * kWarps) * cta * sc.slot_floats, sc.slot_floats, sc.rows, a.c.d, lr, n,
+                  [&](int k) { return k == 0 ? i : 2 * (w + k); }, r);
+      if (done) {
+        write_row<D>(a, row_out<S::kRows>(a, sq, p.h, p.rt, lr), r);
+      } else {
+        constexpr int kCols = Joined<D>::kCols, kVec = kCols < 4 ? kCols : 4;
+        float* q = sc.joined + to;
+        if (lane == 0) *reinterpret_cast<float2*>(q + sc.rows * a.c.d + 2 * lr) = make_float2(r.m, r.l);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const int col = lane * kVec + 32 * (c / kVec * kVec) + c % kVec;
+          if (col < a.c.d) q[lr * a.c.d + col] = r.o[c];
+        }
+      }
     }
-    const int h = static_cast<int>(rest / it.tiles), t0 = static_cast<int>(rest % it.tiles);
-    const int t1 = static_cast<int>(min(int64_t(it.tiles), t0 + (end - at)));
-    const bool whole = t0 == 0 && t1 == it.tiles;
-    // slot 0: the piece that the range starts with, slot 1: the one it ends with
-    float* part = sc.parts + (2 * w + (at == range_start ? 0 : 1)) * sc.slot_floats;
-    Worker<D, RT>::run(a, sq, s, h, rt, t0, t1, whole, part, ring);
-    at += t1 - t0;
-    off += t1 - t0;
   }
 }
 
-// Joins the pieces of the items that several warps shared: one CTA per (row
-// of a tile, row tile and head, sequence); its warps share out the pieces.
-constexpr int kJoinWarps = 4;
-template <int D, int RT>
+// Joins the items that several CTAs shared: one CTA for each that an attention
+// CTA's range ends within, a warp per row.
+constexpr int kJoinWarps = 8;
+template <int D, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-kv_join_kernel(const AttendArgs a, Scratch sc, int limit, int64_t nw) {
-  using S = Shape<D, RT>;
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  __shared__ float s_o[kJoinWarps][D];
+kv_join_kernel(const AttendArgs a, const Scratch sc) {
+  using S = Shape<D, NR>;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int s = blockIdx.z, lr = blockIdx.x;
-  const int rt = blockIdx.y / a.c.heads, h = blockIdx.y % a.c.heads;
-  const Seq sq = load_seq(a.b, s, nullptr);
-  if (sq.n * a.group > limit || rt >= row_tiles<S::kRows>(a, sq)) return;
-  int64_t ts = sc.prefix[s];
-  const int64_t total = sc.prefix[a.b.n_seqs];
-  for (int i = 0; i < rt; ++i) ts += int64_t(row_tile<S::kRows, S::kTile>(a, sq, i).tiles) * a.c.heads;
-  const RowTile it = row_tile<S::kRows, S::kTile>(a, sq, rt);
-  if (lr >= it.rows) return;
-  ts += int64_t(h) * it.tiles;
-  const int64_t te = ts + it.tiles;
-  const int64_t w0 = ((ts + 1) * nw - 1) / total, w1 = (te * nw - 1) / total;  // the warps that own its first and last tile
-  if (w0 == w1) return;  // written whole
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.c.d;
-  constexpr int kCols = D / 32;
-  float o[kCols], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) o[i] = 0.f;
-  for (int64_t w = w0 + warp; w <= w1; w += kJoinWarps) {
-    const int64_t begin = w * total / nw;
-    if (begin >= (w + 1) * total / nw) continue;
-    const float* p = sc.parts + (2 * w + (begin >= ts ? 0 : 1)) * sc.slot_floats + int64_t(lr) * (d + 2);
-    const float pm = p[d], pl = p[d + 1];
-    float v[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) v[i] = lane + 32 * i < d ? p[lane + 32 * i] : 0.f;
-    const float mn = fmaxf(m, pm);
-    const float to = mn == -INFINITY ? 0.f : mn;  // a NaN sum has no maximum and is passed on
-    const float ka = exp2_fast(m - to), kb = exp2_fast(pm - to);
-    l = l * ka + pl * kb;
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = o[i] * ka + v[i] * kb;
-    m = mn;
+  const int c = blockIdx.x;
+  const Open p = sc.open[c];
+  if (!p.any) return;
+  const Seq sq = load_seq(a.b, p.s, nullptr);
+  const int rows = row_tile<S::kRows, S::kTile>(a, sq, p.rt).rows;
+  const Cut cut(p.total, static_cast<int>(p.ctas));
+  int n = 1;
+  while (c + n < p.ctas && cut.first(c + n) < p.te) ++n;
+  for (int lr = threadIdx.x >> 5; lr < rows; lr += kJoinWarps) {
+    Joined<D> r;
+    join_row<D>(sc.joined, sc.slot_floats, sc.rows, a.c.d, lr, n, [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); }, r);
+    write_row<D>(a, row_out<S::kRows>(a, sq, p.h, p.rt, lr), r);
   }
-  if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) s_o[warp][lane + 32 * i] = o[i];
-  __syncthreads();
-  float mn = s_m[0];
-#pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) mn = fmaxf(mn, s_m[i]);
-  const float top = mn == -INFINITY ? 0.f : mn;
-  float ls = 0.f, k[kJoinWarps];
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) k[i] = exp2_fast(s_m[i] - top), ls += s_l[i] * k[i];
-  const int row = rt * S::kRows + lr, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-  const int64_t grow = sq.r0 + qi;
-  const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
-  for (int c = threadIdx.x; c < d; c += kJoinWarps * 32) {
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) x += s_o[i][c] * k[i];
-    a.out[grow * a.out_stride + int64_t(hq) * d + c] = __bfloat16_as_ushort(__float2bfloat16_rn(x * inv));
-  }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[grow * (a.c.heads * a.group) + hq] = ls == 0.f ? -INFINITY : (top + log2f(ls)) * kLn2;
 }
 
 // Sequences with more than `limit` rows (prompts): a warp per item, unsplit.
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, 1)
-kv_attend_rows_kernel(const AttendArgs a, int limit, int row_tiles_max) {
-  using S = Shape<D, RT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+template <int D, int NR>
+__global__ void __launch_bounds__(Shape<D, NR>::kThreads, 1)
+kv_attend_rows_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                      int limit, int row_tiles_max, uint64_t wait_ns) {
+  using S = Shape<D, NR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kWarps = S::kWarps;
+  __shared__ uint64_t s_full[kWarps][S::kStages];
+  __shared__ float2 s_scales[kWarps][S::kStages * S::kGroups];
+  if (threadIdx.x < kWarps * S::kStages) mbar_init(&s_full[0][0] + threadIdx.x, S::kGroups);
+  fence_mbar_init();
+  __syncthreads();
   pdl_launch_dependents();
   pdl_wait_primary();
   const int warp = threadIdx.x >> 5;
@@ -651,53 +838,76 @@ kv_attend_rows_kernel(const AttendArgs a, int limit, int row_tiles_max) {
   const int rt = row_tiles_max - 1 - (blockIdx.x * kWarps + warp);  // long rows first
   if (sq.n * a.group <= limit || rt < 0 || rt >= row_tiles<S::kRows>(a, sq)) return;
   const RowTile it = row_tile<S::kRows, S::kTile>(a, sq, rt);
-  Worker<D, RT>::run(a, sq, s, h, rt, 0, it.tiles, true, nullptr, smem_u32(smem) + warp * S::kWarpBytes);
+  Ring<D, NR> ring{((smem_u32(smem) + 1023u) & ~1023u) + warp * S::kWarpBytes, s_full[warp], s_scales[warp], &map_k, &map_v,
+                   wait_ns, 0, 0};
+  Worker<D, NR>::run(a, sq, s, h, rt, 0, it.tiles, true, Scratch{}, 0, ring);
 }
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-// Rows a tile: 16, or 32 where more are asked for and the accumulators fit.
-int tile_rows(int D, int max_new, int group) { return D < 256 && int64_t(max_new) * group > 16 ? 32 : 16; }
+// Rows a tile, in eights: the fewest that take all of a sequence's rows, up to
+// what the accumulators leave room for.
+int row_eights(int D, int64_t rows) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
+// Sequences with more rows than this go to the kernel for prompts.
+int row_limit(int D) { return D == 256 ? 64 : 128; }
 
-template <int D, int RT>
+template <int D, int NR>
+size_t scratch_shape(const KvCache& c, const KvBatch& b, int group, int sms, Scratch* sc = nullptr, uint8_t* base = nullptr) {
+  using S = Shape<D, NR>;
+  const int rows = part_rows(b.max_new, group, S::kRows), floats = part_floats(rows, c.d);
+  const size_t open = 0, parts = align256(size_t(sms) * sizeof(Open));
+  const size_t joined = parts + align256(size_t(2) * sms * S::kWarps * floats * 4);
+  if (sc) *sc = Scratch{reinterpret_cast<float*>(base + parts), reinterpret_cast<float*>(base + joined),
+                        reinterpret_cast<Open*>(base + open), rows, floats};
+  return joined + align256(size_t(2) * sms * floats * 4);
+}
+
+template <int D, int NR>
 cudaError_t launch_shape(const AttendArgs& a, cudaStream_t stream, int sms) {
-  using S = Shape<D, RT>;
-  cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  using S = Shape<D, NR>;
+  CUtensorMap mk, mv;
+  const uint64_t rows_page = uint64_t(a.c.heads) * a.c.page;
+  cudaError_t e = encode_map_3d(&mk, a.c.k, a.c.d, rows_page, a.c.n_pages, S::kPitch, 16, S::kPitch);
   if (e != cudaSuccess) return e;
-  Scratch sc;
-  sc.prefix = reinterpret_cast<int64_t*>(a.scratch);
-  sc.parts = reinterpret_cast<float*>(a.scratch + align256(size_t(a.b.n_seqs + 1) * 8));
-  sc.slot_floats = part_rows(a.b.max_new, a.group, S::kRows) * (a.c.d + 2);
-  const int limit = 4 * S::kRows;
-  const int64_t rows = int64_t(a.b.max_new) * a.group;
-  if ((e = launch_pdl(kv_attend_kernel<D, RT>, dim3(sms), dim3(kThreads), S::kSmem, stream, a, sc, limit)) != cudaSuccess)
+  if ((e = encode_map_3d(&mv, a.c.v, a.c.d, rows_page, a.c.n_pages, S::kPitch, 16, S::kPitch)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(kv_attend_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem)) != cudaSuccess)
     return e;
-  const int64_t few = rows < limit ? rows : limit;
-  const int nrt = static_cast<int>((few + S::kRows - 1) / S::kRows);
-  const dim3 g(static_cast<unsigned>(few < S::kRows ? few : S::kRows), nrt * a.c.heads, a.b.n_seqs);
-  e = launch_pdl(kv_join_kernel<D, RT>, g, dim3(kJoinWarps * 32), 0, stream, a, sc, limit, int64_t(sms) * kWarps);
+  Scratch sc;
+  scratch_shape<D, NR>(a.c, a.b, a.group, sms, &sc, a.scratch);
+  const int limit = row_limit(D);
+  const int64_t rows = int64_t(a.b.max_new) * a.group;
+  const uint64_t wait = wait_limit_ns();
+  if ((e = launch_pdl(kv_attend_kernel<D, NR>, dim3(sms), dim3(S::kThreads), S::kSmem, stream, a, mk, mv, sc, limit, wait)) !=
+      cudaSuccess)
+    return e;
+  e = launch_pdl(kv_join_kernel<D, NR>, dim3(sms), dim3(kJoinWarps * 32), 0, stream, a, sc);
   if (e != cudaSuccess || rows <= limit) return e;
-  e = cudaFuncSetAttribute(kv_attend_rows_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  e = cudaFuncSetAttribute(kv_attend_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const int all = static_cast<int>((rows + S::kRows - 1) / S::kRows);
-  return launch_pdl(kv_attend_rows_kernel<D, RT>, dim3((all + kWarps - 1) / kWarps, a.c.heads, a.b.n_seqs), dim3(kThreads),
-                    S::kSmem, stream, a, limit, all);
+  return launch_pdl(kv_attend_rows_kernel<D, NR>, dim3((all + S::kWarps - 1) / S::kWarps, a.c.heads, a.b.n_seqs),
+                    dim3(S::kThreads), S::kSmem, stream, a, mk, mv, limit, all, wait);
 }
 
 }  // namespace
 
 size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms) {
-  const int rows = part_rows(b.max_new, group, tile_rows(padded(c.d), b.max_new, group));
-  return align256(size_t(b.n_seqs + 1) * 8) + align256(size_t(2) * sms * kWarps * rows * (c.d + 2) * 4);
+  const int D = padded(c.d), n = row_eights(D, int64_t(b.max_new) * group);
+  if (D == 64) return n == 1 ? scratch_shape<64, 1>(c, b, group, sms) : n == 2 ? scratch_shape<64, 2>(c, b, group, sms)
+                                                                              : scratch_shape<64, 4>(c, b, group, sms);
+  if (D == 128) return n == 1 ? scratch_shape<128, 1>(c, b, group, sms) : n == 2 ? scratch_shape<128, 2>(c, b, group, sms)
+                                                                                : scratch_shape<128, 4>(c, b, group, sms);
+  return n == 1 ? scratch_shape<256, 1>(c, b, group, sms) : scratch_shape<256, 2>(c, b, group, sms);
 }
 
 cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms) {
-  const int D = padded(a.c.d);
-  const bool two = tile_rows(D, a.b.max_new, a.group) == 32;
-  if (D == 64) return two ? launch_shape<64, 2>(a, stream, sms) : launch_shape<64, 1>(a, stream, sms);
-  if (D == 128) return two ? launch_shape<128, 2>(a, stream, sms) : launch_shape<128, 1>(a, stream, sms);
-  return launch_shape<256, 1>(a, stream, sms);
+  const int D = padded(a.c.d), n = row_eights(D, int64_t(a.b.max_new) * a.group);
+  if (D == 64) return n == 1 ? launch_shape<64, 1>(a, stream, sms) : n == 2 ? launch_shape<64, 2>(a, stream, sms)
+                                                                           : launch_shape<64, 4>(a, stream, sms);
+  if (D == 128) return n == 1 ? launch_shape<128, 1>(a, stream, sms) : n == 2 ? launch_shape<128, 2>(a, stream, sms)
+                                                                             : launch_shape<128, 4>(a, stream, sms);
+  return n == 1 ? launch_shape<256, 1>(a, stream, sms) : launch_shape<256, 2>(a, stream, sms);
 }
 
 }  // namespace mq

@@ -104,6 +104,10 @@ void set_last_error(const char* msg);
 cudaError_t encode_map_2d(CUtensorMap* out, const void* base, uint64_t rows, uint64_t row_elems,
                           uint32_t box_inner, uint32_t box_rows, int elem_bytes,
                           int swizzle_bytes = 0);
+// 3-D map over `planes` dense matrices of `rows` x `row_bytes` bytes, box
+// `box_inner` x `box_rows` of one plane, swizzled as above.
+cudaError_t encode_map_3d(CUtensorMap* out, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t planes,
+                          uint32_t box_inner, uint32_t box_rows, int swizzle_bytes);
 int sm_count();
 
 // gamma, beta: per-row clipping factors of Eq. 3, or null for Eq. 1.

@@ -18,6 +18,7 @@ namespace {
 std::mutex g_tm_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::map<std::tuple<const void*, uint64_t, uint64_t, uint32_t, uint32_t, int, int>, CUtensorMap> g_maps;
+std::map<std::tuple<const void*, uint64_t, uint64_t, uint64_t, uint32_t, uint32_t, int>, CUtensorMap> g_maps_3d;
 
 cudaError_t load_encoder() {
   if (g_encode) return cudaSuccess;
@@ -62,6 +63,34 @@ cudaError_t encode_map_2d(CUtensorMap* out, const void* base, uint64_t rows, uin
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   if (g_maps.size() > 4096) g_maps.clear();
   g_maps.emplace(key, m);
+  *out = m;
+  return cudaSuccess;
+}
+
+cudaError_t encode_map_3d(CUtensorMap* out, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t planes,
+                          uint32_t box_inner, uint32_t box_rows, int swizzle_bytes) {
+  if (swizzle_bytes != 64 && swizzle_bytes != 128) return cudaErrorInvalidValue;
+  std::lock_guard<std::mutex> lk(g_tm_mutex);
+  auto key = std::make_tuple(base, row_bytes, rows, planes, box_inner, box_rows, swizzle_bytes);
+  auto it = g_maps_3d.find(key);
+  if (it != g_maps_3d.end()) {
+    *out = it->second;
+    return cudaSuccess;
+  }
+  cudaError_t e = load_encoder();
+  if (e != cudaSuccess) return e;
+  CUtensorMap m;
+  const cuuint64_t dims[3] = {row_bytes, rows, planes};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * rows};
+  const cuuint32_t box[3] = {box_inner, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  if (g_maps_3d.size() > 4096) g_maps_3d.clear();
+  g_maps_3d.emplace(key, m);
   *out = m;
   return cudaSuccess;
 }

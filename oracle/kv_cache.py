@@ -36,10 +36,11 @@ def values(codes: np.ndarray, scales: np.ndarray, page: int) -> np.ndarray:
     return codes.astype(np.float64) * np.repeat(scales.astype(np.float64), page)[:len(codes), None]
 
 
-def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, places, scale: float, softcap: float = 0.0, window: int = 0):
+def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, v_scales, places, scale: float, softcap: float = 0.0,
+           window: int = 0):
     """One head: q (rows, dim) at `places`, k and v (tokens, dim), float64.
-    Returns (out, lse, weight of |v|): the last is sum_j p_j |v_j|, for the
-    tolerances."""
+    Returns (out, lse, sum_j p_j |v_j|, sum_j p_j 383 s_j): the last two, with s
+    the tokens' V scales, for the tolerances."""
     s = q @ k.T * scale
     if softcap:
         s = softcap * np.tanh(s / softcap)
@@ -47,7 +48,7 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, places, scale: float, so
     at = np.asarray(places)[:, None]
     seen = (j <= at) & ((j > at - window) if window else True)
     out, mass = np.zeros((len(q), v.shape[1])), np.zeros((len(q), v.shape[1]))
-    lse = np.full(len(q), -math.inf)
+    lse, gross = np.full(len(q), -math.inf), np.zeros(len(q))
     for r in range(len(q)):
         if seen[r].any():
             x = s[r][seen[r]]
@@ -56,31 +57,38 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, places, scale: float, so
             p = e / e.sum()
             out[r], mass[r] = p @ v[seen[r]], p @ np.abs(v[seen[r]])
             lse[r] = top + math.log(e.sum())
-    return out, lse, mass
+            gross[r] = 383 * (p @ v_scales[seen[r]])
+    return out, lse, mass, gross
 
 
-def score_error(q: np.ndarray, k: np.ndarray, scale: float, softcap: float) -> np.ndarray:
-    """Bound per row on the error of any score computed in fp32 from exact q
-    and k: the products' sum (a tensor core may cut each of its dim / 16 + 16
-    steps by 2 u of the magnitudes), the three scalings 3 u, and for the cap
-    4 u of its range. u = 2^-24. A query's values below 2^-25 of its largest are
-    lost: 2^-25 dim |k|max |q|max."""
+def score_error(q: np.ndarray, unit: float, scale: float, softcap: float) -> np.ndarray:
+    """Bound per row on the error of any score computed in fp32 from exact q and
+    codes of a scale of at most `unit`. The sums run over q (code + 128), from
+    -128 sum(q): no partial sum exceeds 255 unit |q|_1, and each of the dim / 16
+    + 16 steps (a tensor core may cut a step by 2 u of that) and of the dim / 4 + 4
+    additions of sum(q) costs of it; the scalings 6 u. For the cap 4 u of its range,
+    twice. u = 2^-24. A query's values below 2^-25 of its largest are lost:
+    2^-25 dim 127 unit |q|max."""
     u, dim = 2.0 ** -24, q.shape[1]
-    big = np.max(np.abs(q) @ np.abs(k).T, axis=1) if len(k) else np.zeros(len(q))
-    lost = 2.0 ** -25 * dim * np.max(np.abs(q), axis=1) * (np.max(np.abs(k)) if len(k) else 0.0)
-    return abs(scale) * (big * (2 * (dim / 16 + 16) + 6) * u + lost) + (8 * u * softcap)
+    big = 255 * unit * np.sum(np.abs(q), axis=1)
+    lost = 2.0 ** -25 * dim * np.max(np.abs(q), axis=1) * 127 * unit
+    return abs(scale) * (big * (2 * (dim / 16 + 16) + dim / 4 + 4 + 6) * u + lost) + (8 * u * softcap)
 
 
-def out_error(out: np.ndarray, mass: np.ndarray, v: np.ndarray, delta: np.ndarray, tokens: int) -> np.ndarray:
+def out_error(out: np.ndarray, mass: np.ndarray, gross: np.ndarray, unit: float, delta: np.ndarray, tokens: int) -> np.ndarray:
     """Bound on the bf16 output's error: its own rounding 2^-8 |o|; each
     probability off by e^delta twice (itself and the sum), its exponential
-    2^-21, its fp16 rounding 2^-11; the running sums (2 u a step of 16 tokens
-    and of every rescaling, at most one a step); probabilities below 2^-29 of the
-    largest lose 2^-39 of it absolutely, a token each."""
+    2^-21, its fp16 rounding 2^-11: of `mass`, the sum of p |v|. The running sums
+    take the byte, code + 128, and then 128 times the probabilities away: 8 u a step
+    of 16 tokens and of the joining, of `gross`, the sum of p (255 + 128) s with s the
+    scale of the value's page. Probabilities below 2^-22 of the running maximum,
+    which is at most the largest, are fp16 subnormals: half a step there is 2^-25 of
+    the factor 2^-8 they stand high, 2^-33 of the largest, a token each, times its
+    code and `unit`, the largest scale of V (which their ratio was taken to)."""
     u = 2.0 ** -24
-    rel = 2 * np.expm1(delta)[:, None] + 2.0 ** -20 + 2.0 ** -11 + 8 * u * (tokens / 16 + 8)
-    under = tokens * 2.0 ** -39 * (np.max(np.abs(v)) if len(v) else 0.0)
-    return (2.0 ** -8 * np.abs(out) + rel * mass + under) * (1 + 2.0 ** -8)
+    rel = 2 * np.expm1(delta)[:, None] + 2.0 ** -20 + 2.0 ** -11
+    under = tokens * 2.0 ** -33 * 127 * unit
+    return (2.0 ** -8 * np.abs(out) + rel * mass + 8 * u * (tokens / 16 + 32) * gross[:, None] + under) * (1 + 2.0 ** -8)
 
 
 def lse_error(lse: np.ndarray, delta: np.ndarray, tokens: int) -> np.ndarray:

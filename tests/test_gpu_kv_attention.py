@@ -42,12 +42,14 @@ def check(b, hq, q, out, log, softcap=0.0, window=0, scale=None, gap=0, rows=Non
         r0 = b.starts[s]
         pick = np.arange(n) if rows is None else np.array([r for r in rows if r < n], dtype=int)
         for h in range(b.heads):
-            k, v = (okv.values(*b.tokens(w, s, h, c), b.page) for w in range(2))
+            (kc, ks), (vc, vs) = (b.tokens(w, s, h, c) for w in range(2))
+            k, v = okv.values(kc, ks, b.page), okv.values(vc, vs, b.page)
+            of_token = np.repeat(vs.astype(np.float64), b.page)[:c]
             for a in range(h * group, (h + 1) * group):
                 x = q64[r0:r0 + n, a][pick]
-                o, l, mass = okv.attend(x, k, v, b.places(s)[pick], scale, softcap, window)
-                delta = okv.score_error(x, k, scale, softcap)
-                tol = okv.out_error(o, mass, v, delta, c)
+                o, l, mass, gross = okv.attend(x, k, v, of_token, b.places(s)[pick], scale, softcap, window)
+                delta = okv.score_error(x, ks.max(initial=0.0), scale, softcap)
+                tol = okv.out_error(o, mass, gross, vs.max(initial=0.0), delta, c)
                 err = np.abs(got[r0:r0 + n, a * dim:(a + 1) * dim][pick] - o)
                 assert np.all(err <= tol), (s, a, (err / np.maximum(tol, 1e-30)).max())
                 worst = max(worst, (err / np.maximum(tol, 1e-30)).max(initial=0.0))
