@@ -106,6 +106,10 @@ struct Shape {
   static constexpr int kStages = 3;
   static constexpr int kTile = D * kWarps <= 1024 ? 32 : 16;  // tokens a stage
   static constexpr int kGroups = kTile / 16;
+  // What an item costs beside its tiles, in tiles: a warp's start on an item (lengths, pages, queries, first
+  // bytes, one after another) takes about as long as two 16-token tiles of a busy card. Without it one warp got
+  // all 24 items of three idle rows and kept the others waiting: 168 us against 112 at 64 sequences of up to 8192.
+  static constexpr int kStart = 32 / kTile;
   static constexpr int kPitch = D == 64 ? 64 : 128;
   static constexpr int kBoxes = D / kPitch;
   static constexpr int kBoxBytes = 16 * kPitch;
@@ -137,19 +141,24 @@ struct RowTile {
   int lo;       // first token that some row sees
   int j0, j1;   // lo rounded down to a tile, and the end of the tokens seen
   int tiles;    // at least 1
+  int units;    // what it counts in the split
+  int start;    // units before the first tile
 };
-template <int ROWS, int TILE>
+template <int ROWS, int TILE, int START>
 __device__ __forceinline__ RowTile row_tile(const AttendArgs& a, const Seq& s, int rt) {
   RowTile t;
   const int first = rt * ROWS, all = s.n * a.group;
   t.rows = min(ROWS, all - first);
-  t.i0 = first / a.group;
-  const int i1 = (first + t.rows - 1) / a.group;
+  const bool one = all <= ROWS;  // the usual case, without the divisions
+  t.i0 = one ? 0 : first / a.group;
+  const int i1 = one ? s.n - 1 : (first + t.rows - 1) / a.group;
   const int base = s.len - s.n;
   t.j1 = max(base + i1 + 1, 0);
   t.lo = a.window > 0 ? max(base + t.i0 - a.window + 1, 0) : 0;
   t.j0 = t.lo & ~(TILE - 1);
   t.tiles = max((t.j1 - t.j0 + TILE - 1) / TILE, 1);
+  t.start = t.j1 > 0 ? START : 0;
+  t.units = t.tiles + t.start;
   return t;
 }
 template <int ROWS>
@@ -160,17 +169,16 @@ __device__ __forceinline__ int row_tiles(const AttendArgs& a, const Seq& s) {
 // Partial sums of a piece of a shared item: per row the d outputs before the
 // division, then (maximum, sum of exponentials), base 2.
 struct Scratch {
-  float* parts;   // 2 slots a warp: the piece its range starts with, the one it ends with
-  float* joined;  // 2 slots a CTA, the same over its warps
+  float* parts;   // a slot a warp: the piece its range starts with, where it goes on behind it
+  float* joined;  // 2 slots a CTA, over its warps: the piece its range starts with, the one it ends with
   struct Open* open;  // a CTA each
   int rows;       // rows a slot holds
   int slot_floats;
 };
 // The item that a CTA's range ends within, if it starts in that CTA.
 struct Open {
-  int s, rt, h, any;
-  int64_t ts, te;
-  int64_t total, ctas;
+  int r0, first_row, h, rows;  // the sequence's first row, the tile's in it, its rows (0: none)
+  int n;                       // CTAs that share the item
 };
 
 __host__ __device__ __forceinline__ int part_rows(int max_new, int group, int rows) {
@@ -192,6 +200,11 @@ struct Cut {
     }
   }
   __device__ __forceinline__ int64_t first(int i) const { return each * i + min(i, rest); }
+  __device__ __forceinline__ int part(int64_t x) const {  // that holds x
+    const int64_t longer = (each + 1) * rest, y = x < longer ? x : x - longer, by = x < longer ? each + 1 : each;
+    const int64_t q = (y | by) <= 0x7fffffff ? static_cast<uint32_t>(y) / static_cast<uint32_t>(by) : y / by;
+    return static_cast<int>(q) + (x < longer ? 0 : rest);
+  }
 };
 
 // Where an item's row goes.
@@ -199,10 +212,10 @@ struct RowOut {
   int64_t row;
   int head;
 };
-template <int ROWS>
-__device__ __forceinline__ RowOut row_out(const AttendArgs& a, const Seq& sq, int h, int rt, int lr) {
-  const int row = rt * ROWS + lr, qi = row / a.group;
-  return RowOut{int64_t(sq.r0) + qi, h * a.group + row - qi * a.group};
+// row: of its sequence, the first of which is r0.
+__device__ __forceinline__ RowOut row_out(const AttendArgs& a, int r0, int h, int row) {
+  const int qi = row / a.group;
+  return RowOut{int64_t(r0) + qi, h * a.group + row - qi * a.group};
 }
 
 template <int D, int NR>
@@ -211,13 +224,23 @@ struct Worker {
   static constexpr int kMt = D / 16;  // m-tiles of the output
   static constexpr int kJ = D / 64;   // 64-value steps of a key
 
-  // One warp's pass over tiles [t0, t1) of an item. False: a wait gave up.
+  // One warp's pass over tiles [t0, t1) of an item; its sums go to `part` (of
+  // part_rows rows), or, if that is null, the item's outputs. False: a wait gave up.
   static __device__ __forceinline__ bool run(const AttendArgs& a, const Seq& sq, int s, int h, int rt, int t0, int t1,
-                                             bool whole, const Scratch& scr, int slot, Ring<D, NR>& ring) {
+                                             float* part, int part_rows, Ring<D, NR>& ring) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const RowTile it = row_tile<S::kRows, S::kTile>(a, sq, rt);
+    const RowTile it = row_tile<S::kRows, S::kTile, S::kStart>(a, sq, rt);
     const int d = a.c.d, chunks = d >> 4;
     const int first_row = rt * S::kRows;
+    if (it.j1 == 0) {  // no row sees a token
+      for (int lr = 0; lr < it.rows; ++lr) {
+        const RowOut ro = row_out(a, sq.r0, h, first_row + lr);
+        if (lane < 2 * chunks)
+          *reinterpret_cast<uint4*>(a.out + ro.row * a.out_stride + int64_t(ro.head) * d + 8 * lane) = make_uint4(0, 0, 0, 0);
+        if (a.lse && lane == 0) a.lse[ro.row * (a.c.heads * a.group) + ro.head] = -INFINITY;
+      }
+      return true;
+    }
 
     // ---- the ring: lane i holds the page of index page0 + i and its scales, and starts its copies
     const int page = a.c.page, log2p = a.c.page_log2;
@@ -241,19 +264,18 @@ struct Worker {
             }
           }
           if (lane == index - page0) {
-            *sc = mine;
             if (pid >= 0) {
               const uint32_t kb = ring.base + stage * S::kStageBytes + gi * S::kGroupBytes, vb = kb + 16 * D;
               const int row = h * page + (j & (page - 1));
-              mbar_arrive_expect_tx(bar, S::kGroupBytes);
+              mbar_expect_tx(bar, S::kGroupBytes);
 #pragma unroll
               for (int x = 0; x < S::kBoxes; ++x) {
                 tma_load_3d(kb + x * S::kBoxBytes, ring.map_k, 128 * x, row, pid, bar);
                 tma_load_3d(vb + x * S::kBoxBytes, ring.map_v, 128 * x, row, pid, bar);
               }
-            } else {
-              mbar_arrive(bar);
             }
+            *sc = mine;  // waits for the scales; the copies are on their way
+            mbar_arrive(bar);
           }
         } else if (lane == 0) {
           *sc = make_float2(0.f, -1.f);
@@ -261,6 +283,20 @@ struct Worker {
         }
       }
     };
+    uint4 raw[NR][kJ][2];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int lr = 8 * r + g, row = first_row + lr, qi = row / a.group, hg = row - qi * a.group;
+      const uint16_t* qp = a.q + (sq.r0 + qi) * a.q_stride + int64_t(h * a.group + hg) * d;
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const int c = 4 * j + t;
+        const bool in = lr < it.rows && c < chunks;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          raw[r][j][k] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
+      }
+    }
     const int stage0 = ring.stage;
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) {
@@ -279,19 +315,12 @@ struct Worker {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int lr = 8 * r + g;
-      const bool ok = lr < it.rows;
-      const int row = first_row + lr, qi = row / a.group, hg = row - qi * a.group;
-      const uint16_t* qp = a.q + (sq.r0 + qi) * a.q_stride + int64_t(h * a.group + hg) * d;
-      uint4 raw[kJ][2];
       float mx = 0.f;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
-        const int c = 4 * j + t;
-        const bool in = ok && c < chunks;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          raw[j][k] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
+          const uint32_t w[4] = {raw[r][j][k].x, raw[r][j][k].y, raw[r][j][k].z, raw[r][j][k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
@@ -303,13 +332,13 @@ struct Worker {
       ex = ex < 1 || ex > 253 ? 127 : ex;
       const float down = __int_as_float((254 - ex) << 23) * sign;
       const float up = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
-      const int pl = ok ? sq.len - sq.n + qi : -1;
+      const int pl = lr < it.rows ? sq.len - sq.n + (first_row + lr) / a.group : -1;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t w[4] = {raw[j][k].x, raw[j][k].y, raw[j][k].z, raw[j][k].w};
+          const uint32_t w[4] = {raw[r][j][k].x, raw[r][j][k].y, raw[r][j][k].z, raw[r][j][k].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // values 8 k + 2 i, + 1 of the chunk: product 4 j + 2 k + i / 2, half i % 2
             const uint32_t h2 = f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
@@ -522,10 +551,9 @@ struct Worker {
         const int lr = 8 * r + 2 * t + e;
         if (lr >= it.rows) continue;
         auto value = [&](int i, int half) { return (o[r][i][2 * half + e] - ps[r][e]) * kBack; };
-        if (!whole) {
-          float* p = scr.parts + int64_t(slot) * scr.slot_floats;
-          if (g == 0) *reinterpret_cast<float2*>(p + scr.rows * d + 2 * lr) = make_float2(m[r][e], l[r][e]);
-          p += lr * d;
+        if (part) {
+          if (g == 0) *reinterpret_cast<float2*>(part + part_rows * d + 2 * lr) = make_float2(m[r][e], l[r][e]);
+          float* p = part + lr * d;
 #pragma unroll
           for (int i = 0; i < kMt; i += 2) {
             const int col = kRun * g + 2 * (i % 8) + 128 * (i / 8);
@@ -535,7 +563,7 @@ struct Worker {
           }
           continue;
         }
-        const RowOut ro = row_out<S::kRows>(a, sq, h, rt, lr);
+        const RowOut ro = row_out(a, sq.r0, h, first_row + lr);
         const float inv = l[r][e] > 0.f ? vmax / l[r][e] : (l[r][e] == 0.f ? 0.f : l[r][e]);
         if (a.lse && g == 0)
           a.lse[ro.row * (a.c.heads * a.group) + ro.head] = l[r][e] == 0.f ? -INFINITY : (m[r][e] + log2f(l[r][e])) * kLn2;
@@ -567,31 +595,53 @@ struct Worker {
   }
 };
 
-// Joins one row of n pieces (piece i in slot slot_of(i)), in their order, by one
+// Joins one row of n pieces (piece i at sums_of(i)), in their order, by one
 // warp: the pieces' weights first, a lane each, then the sums.
 template <int D>
 struct Joined {
   static constexpr int kCols = D / 32;
   float o[kCols], m, l;
 };
-template <int D, typename SlotOf>
-__device__ __forceinline__ void join_row(const float* parts, int slot_floats, int rows, int d, int lr, int n, SlotOf slot_of,
-                                         Joined<D>& r) {
+template <int D, typename SumsOf>
+__device__ __forceinline__ void join_row(int rows, int d, int lr, int n, SumsOf sums_of, Joined<D>& r) {
   constexpr int kCols = Joined<D>::kCols, kVec = kCols < 4 ? kCols : 4;
   const int lane = threadIdx.x & 31;
   r.m = -INFINITY;
   r.l = 0.f;
 #pragma unroll
   for (int i = 0; i < kCols; ++i) r.o[i] = 0.f;
+  constexpr int kBatch = 32 / kCols;
   for (int first = 0; first < n; first += 32) {
     const bool have = first + lane < n;
-    const int64_t mine = have ? int64_t(slot_of(first + lane)) * slot_floats : 0;
-    const float2 ml = have ? __ldcg(reinterpret_cast<const float2*>(parts + mine + rows * d + 2 * lr)) : make_float2(-INFINITY, 0.f);
+    const float* mine = have ? sums_of(first + lane) : nullptr;
+    const float2 ml = have ? *reinterpret_cast<const float2*>(mine + rows * d + 2 * lr) : make_float2(-INFINITY, 0.f);
+    const int count = min(32, n - first);
+    float v[kBatch][kCols];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float* p =
+            reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (k0 + k) & 31)) + lr * d;
+#pragma unroll
+        for (int i = 0; i < kCols; i += kVec) {
+          const int col = lane * kVec + 32 * i;
+          const bool in = k0 + k < count && col < d;
+          if constexpr (kVec == 4) {
+            const float4 x = in ? *reinterpret_cast<const float4*>(p + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[k][i] = x.x, v[k][i + 1] = x.y, v[k][i + 2] = x.z, v[k][i + 3] = x.w;
+          } else {
+            const float2 x = in ? *reinterpret_cast<const float2*>(p + col) : make_float2(0.f, 0.f);
+            v[k][i] = x.x, v[k][i + 1] = x.y;
+          }
+        }
+      }
+    };
+    load(0);
     float top = fmaxf(r.m, ml.x);
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
     const float to = top == -INFINITY ? 0.f : top;  // a NaN sum has no maximum and is passed on
-    const float keep = exp2_fast(r.m - to), weight = exp2_fast(ml.x - to);
+    const float keep = exp2_fast(r.m - to), weight = have ? exp2_fast(ml.x - to) : 0.f;
     float sum = ml.y * weight;
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
@@ -599,33 +649,15 @@ __device__ __forceinline__ void join_row(const float* parts, int slot_floats, in
     r.m = top;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) r.o[i] *= keep;
-    const int count = min(32, n - first);
-    constexpr int kBatch = D == 256 ? 4 : 8;
-    for (int k0 = 0; k0 < count; k0 += kBatch) {
-      float v[kBatch][kCols], wt[kBatch];
+    for (int k0 = 0;;) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const bool ok = k0 + k < count;
-        const float* p = parts + __shfl_sync(0xffffffffu, mine, (k0 + k) & 31) + lr * d;
         const float w = __shfl_sync(0xffffffffu, weight, (k0 + k) & 31);
-        wt[k] = ok ? w : 0.f;
 #pragma unroll
-        for (int i = 0; i < kCols; i += kVec) {
-          const int col = lane * kVec + 32 * i;
-          const bool in = ok && col < d;
-          if constexpr (kVec == 4) {
-            const float4 x = in ? __ldcg(reinterpret_cast<const float4*>(p + col)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[k][i] = x.x, v[k][i + 1] = x.y, v[k][i + 2] = x.z, v[k][i + 3] = x.w;
-          } else {
-            const float2 x = in ? __ldcg(reinterpret_cast<const float2*>(p + col)) : make_float2(0.f, 0.f);
-            v[k][i] = x.x, v[k][i + 1] = x.y;
-          }
-        }
+        for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(k0 + k < count ? w : 0.f, v[k][i], r.o[i]);
       }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(wt[k], v[k][i], r.o[i]);
+      if ((k0 += kBatch) >= count) break;
+      load(k0);
     }
   }
 }
@@ -660,7 +692,7 @@ __device__ __forceinline__ int64_t seq_tiles(const AttendArgs& a, const Seq& s, 
   if (s.n * a.group > limit) return 0;
   int64_t t = 0;
   const int nrt = row_tiles<S::kRows>(a, s);
-  for (int rt = 0; rt < nrt; ++rt) t += row_tile<S::kRows, S::kTile>(a, s, rt).tiles;
+  for (int rt = 0; rt < nrt; ++rt) t += row_tile<S::kRows, S::kTile, S::kStart>(a, s, rt).units;
   return t * a.c.heads;
 }
 
@@ -675,14 +707,18 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
   __shared__ int64_t s_warp[kWarps];
   __shared__ uint64_t s_full[kWarps][S::kStages];
   __shared__ float2 s_scales[kWarps][S::kStages * S::kGroups];
-  struct Piece {  // an unfinished piece of a warp
-    int64_t ts, te, begin;  // its item's tiles, and where the piece begins
-    int s, rt, h, any;
+  struct Piece {  // an unfinished piece of a warp: the one its range starts with, the one it ends with
+    const float* sums;
+    int64_t te;          // the end of its item's tiles
+    int r0, first_row, h;
+    int rows;            // 0: none
+    bool starts, leads;  // its item starts in this CTA; it is its item's first piece here
   };
   __shared__ Piece s_piece[2 * kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < kWarps * S::kStages) mbar_init(&s_full[0][0] + tid, S::kGroups);
-  if (tid < 2 * kWarps) s_piece[tid].any = 0;
+  if (tid < 2 * kWarps) s_piece[tid].rows = 0;
+  if (tid == 0) prefetch_tmap(&map_k), prefetch_tmap(&map_v);
   fence_mbar_init();
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -699,16 +735,21 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  int64_t before = 0;
-  for (int i = 0; i < warp; ++i) before += s_warp[i];
+  int64_t sums = lane < kWarps ? s_warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += up;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+  const int64_t before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, sums, warp - 1);
   s_pre[tid + 1] = before + inc;
   if (tid == 0) s_pre[0] = 0;
   __syncthreads();
-  const int64_t total = s_pre[kThreads];
   // ---- this CTA's range (a tile a warp at least), and this warp's
   const int cta = blockIdx.x;
   const int ctas = static_cast<int>(min(int64_t(gridDim.x), max((total + kWarps - 1) / kWarps, int64_t(1))));
-  if (tid == 0) sc.open[cta].any = 0;
+  if (tid == 0) sc.open[cta].rows = 0;
   if (cta >= ctas || total == 0) return;
   const Cut cut_ctas(total, ctas);
   const int64_t A = cut_ctas.first(cta), B = cut_ctas.first(cta + 1);
@@ -716,10 +757,9 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
   int64_t at = A + cut.first(warp);
   const int64_t end = A + cut.first(warp + 1);
   if (at < end) {
-    int run = 0;
-#pragma unroll
-    for (int step = kThreads / 2; step > 0; step >>= 1)
-      if (s_pre[run + step] <= at) run += step;
+    // the last run that starts at or before `at`
+    int run = (__popc(__ballot_sync(0xffffffffu, s_pre[lane * kWarps] <= at)) - 1) * kWarps;
+    run += __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_pre[run + lane] <= at)) - 1;
     int s = run * per;
     int64_t off = at - s_pre[run];
     Seq sq = load_seq(a.b, s, nullptr);
@@ -743,78 +783,103 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
       }
       int rt = 0;
       int64_t rest = off;
-      RowTile it = row_tile<S::kRows, S::kTile>(a, sq, 0);
-      while (rest >= int64_t(it.tiles) * a.c.heads) {
-        rest -= int64_t(it.tiles) * a.c.heads;
-        it = row_tile<S::kRows, S::kTile>(a, sq, ++rt);
+      RowTile it = row_tile<S::kRows, S::kTile, S::kStart>(a, sq, 0);
+      while (rest >= int64_t(it.units) * a.c.heads) {
+        rest -= int64_t(it.units) * a.c.heads;
+        it = row_tile<S::kRows, S::kTile, S::kStart>(a, sq, ++rt);
       }
-      const int h = static_cast<int>(rest / it.tiles), t0 = static_cast<int>(rest % it.tiles);
-      const int t1 = static_cast<int>(min(int64_t(it.tiles), t0 + (end - at)));
+      const int units = it.units;
+      const int h = static_cast<int>(rest <= 0x7fffffff ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(units) : rest / units);
+      const int u0 = static_cast<int>(rest - int64_t(h) * units);
+      const int u1 = static_cast<int>(min(int64_t(units), u0 + (end - at)));
+      const int t0 = max(u0 - it.start, 0), t1 = max(u1 - it.start, 0);
+      const int64_t ts = at - u0 + it.start;  // the item's first tile
       const bool whole = t0 == 0 && t1 == it.tiles;
-      const int slot = 2 * warp + (at == begin ? 0 : 1);
-      if (!whole && lane == 0) s_piece[slot] = Piece{at - t0, at - t0 + it.tiles, at, s, rt, h, 1};
-      if (!Worker<D, NR>::run(a, sq, s, h, rt, t0, t1, whole, sc, 2 * kWarps * cta + slot, ring)) break;
-      at += t1 - t0;
-      off += t1 - t0;
+      if (t0 < t1) {
+        // a piece that ends the range stays in the ring, which is then free
+        float* part = at + (u1 - u0) == end ? reinterpret_cast<float*>(smem + (ring.base - smem_u32(smem)))
+                                            : sc.parts + int64_t(kWarps * cta + warp) * sc.slot_floats;
+        if (!whole && lane == 0)
+          s_piece[2 * warp + (at == begin ? 0 : 1)] =
+              Piece{part, ts + it.tiles, sq.r0, rt * S::kRows, h, it.rows, ts >= A, t0 == 0 || ts + t0 == A};
+        if (!Worker<D, NR>::run(a, sq, s, h, rt, t0, t1, whole ? nullptr : part, sc.rows, ring)) break;
+      }
+      at += u1 - u0;
+      off += u1 - u0;
     }
   }
   // ---- pieces of one item in this CTA become one, or the item's outputs
   __syncthreads();
+  const bool leads = lane < 2 * kWarps && s_piece[lane].rows > 0 && s_piece[lane].leads;
   int task = 0;
-  for (int i = 0; i < 2 * kWarps; ++i) {
+  for (unsigned left = __ballot_sync(0xffffffffu, leads); left; left &= left - 1) {
+    const int i = __ffs(left) - 1, w = i >> 1;
     const Piece p = s_piece[i];
-    if (!p.any || p.begin != max(p.ts, A)) continue;  // the first of its item here
-    const int w = i >> 1;
-    int n = 1;  // the others: what the next warps' ranges start with
-    while (w + n < kWarps && A + cut.first(w + n) < min(p.te, B)) ++n;
-    const Seq sq = load_seq(a.b, p.s, nullptr);
-    const int rows = row_tile<S::kRows, S::kTile>(a, sq, p.rt).rows;
-    const bool done = p.ts >= A && p.te <= B;
-    const int64_t to = int64_t(2 * cta + (p.ts < A ? 0 : 1)) * sc.slot_floats;
-    if (p.ts >= A && p.te > B && tid == 0) sc.open[cta] = Open{p.s, p.rt, p.h, 1, p.ts, p.te, total, ctas};
-    for (int lr = 0; lr < rows; ++lr) {
+    // the others: what the next warps' ranges start with
+    const int n = cut.part(min(p.te, B) - 1 - A) - w + 1;
+    float* to = sc.joined + int64_t(2 * cta + (p.starts ? 1 : 0)) * sc.slot_floats;
+    if (p.starts && p.te > B && tid == 0) sc.open[cta] = Open{p.r0, p.first_row, p.h, p.rows, cut_ctas.part(p.te - 1) - cta + 1};
+    for (int lr = 0; lr < p.rows; ++lr) {
       if (task++ % kWarps != warp) continue;
       Joined<D> r;
-      join_row<D>(sc.parts + int64_t(2 * kWarps) * cta * sc.slot_floats, sc.slot_floats, sc.rows, a.c.d, lr, n,
-                  [&](int k) { return k == 0 ? i : 2 * (w + k); }, r);
-      if (done) {
-        write_row<D>(a, row_out<S::kRows>(a, sq, p.h, p.rt, lr), r);
+      join_row<D>(sc.rows, a.c.d, lr, n, [&](int k) { return s_piece[k == 0 ? i : 2 * (w + k)].sums; }, r);
+      if (p.starts && p.te <= B) {
+        write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
       } else {
         constexpr int kCols = Joined<D>::kCols, kVec = kCols < 4 ? kCols : 4;
-        float* q = sc.joined + to;
-        if (lane == 0) *reinterpret_cast<float2*>(q + sc.rows * a.c.d + 2 * lr) = make_float2(r.m, r.l);
+        if (lane == 0) *reinterpret_cast<float2*>(to + sc.rows * a.c.d + 2 * lr) = make_float2(r.m, r.l);
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const int col = lane * kVec + 32 * (c / kVec * kVec) + c % kVec;
-          if (col < a.c.d) q[lr * a.c.d + col] = r.o[c];
+        for (int c = 0; c < kCols; c += kVec) {
+          const int col = lane * kVec + 32 * c;
+          if (col >= a.c.d) continue;
+          if constexpr (kVec == 4)
+            *reinterpret_cast<float4*>(to + lr * a.c.d + col) = make_float4(r.o[c], r.o[c + 1], r.o[c + 2], r.o[c + 3]);
+          else
+            *reinterpret_cast<float2*>(to + lr * a.c.d + col) = make_float2(r.o[c], r.o[c + 1]);
         }
       }
     }
   }
 }
 
-// Joins the items that several CTAs shared: one CTA for each that an attention
-// CTA's range ends within, a warp per row.
-constexpr int kJoinWarps = 8;
-template <int D, int NR>
+// Joins the items that several CTAs shared: one CTA for each row of an item that
+// an attention CTA's range ends within. Its warps take a run of the pieces each.
+constexpr int kJoinWarps = 4;
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 kv_join_kernel(const AttendArgs a, const Scratch sc) {
-  using S = Shape<D, NR>;
+  constexpr int kCols = Joined<D>::kCols;
+  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, lr = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Open p = sc.open[c];
-  if (!p.any) return;
-  const Seq sq = load_seq(a.b, p.s, nullptr);
-  const int rows = row_tile<S::kRows, S::kTile>(a, sq, p.rt).rows;
-  const Cut cut(p.total, static_cast<int>(p.ctas));
-  int n = 1;
-  while (c + n < p.ctas && cut.first(c + n) < p.te) ++n;
-  for (int lr = threadIdx.x >> 5; lr < rows; lr += kJoinWarps) {
-    Joined<D> r;
-    join_row<D>(sc.joined, sc.slot_floats, sc.rows, a.c.d, lr, n, [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); }, r);
-    write_row<D>(a, row_out<S::kRows>(a, sq, p.h, p.rt, lr), r);
+  if (lr >= p.rows) return;
+  const int run = (p.n + kJoinWarps - 1) / kJoinWarps, first = warp * run;
+  Joined<D> r;
+  join_row<D>(sc.rows, a.c.d, lr, min(run, p.n - first),
+              [&](int k) { return sc.joined + int64_t(2 * (c + first + k) + (first + k == 0 ? 1 : 0)) * sc.slot_floats; }, r);
+  if (warp > 0) {
+    if (lane == 0) s_m[warp] = r.m, s_l[warp] = r.l;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) s_o[warp][lane + 32 * i] = r.o[i];
   }
+  __syncthreads();
+  if (warp > 0) return;
+  float top = r.m;
+  for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
+  const float to = top == -INFINITY ? 0.f : top, keep = exp2_fast(r.m - to);
+  r.m = top;
+  r.l *= keep;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) r.o[i] *= keep;
+  for (int k = 1; k < kJoinWarps; ++k) {
+    const float w = exp2_fast(s_m[k] - to);
+    r.l = fmaf(s_l[k], w, r.l);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(s_o[k][lane + 32 * i], w, r.o[i]);
+  }
+  write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
 }
 
 // Sequences with more than `limit` rows (prompts): a warp per item, unsplit.
@@ -837,10 +902,10 @@ kv_attend_rows_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap ma
   const Seq sq = load_seq(a.b, s, nullptr);
   const int rt = row_tiles_max - 1 - (blockIdx.x * kWarps + warp);  // long rows first
   if (sq.n * a.group <= limit || rt < 0 || rt >= row_tiles<S::kRows>(a, sq)) return;
-  const RowTile it = row_tile<S::kRows, S::kTile>(a, sq, rt);
+  const RowTile it = row_tile<S::kRows, S::kTile, S::kStart>(a, sq, rt);
   Ring<D, NR> ring{((smem_u32(smem) + 1023u) & ~1023u) + warp * S::kWarpBytes, s_full[warp], s_scales[warp], &map_k, &map_v,
                    wait_ns, 0, 0};
-  Worker<D, NR>::run(a, sq, s, h, rt, 0, it.tiles, true, Scratch{}, 0, ring);
+  Worker<D, NR>::run(a, sq, s, h, rt, 0, it.tiles, nullptr, 0, ring);
 }
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -857,7 +922,7 @@ size_t scratch_shape(const KvCache& c, const KvBatch& b, int group, int sms, Scr
   using S = Shape<D, NR>;
   const int rows = part_rows(b.max_new, group, S::kRows), floats = part_floats(rows, c.d);
   const size_t open = 0, parts = align256(size_t(sms) * sizeof(Open));
-  const size_t joined = parts + align256(size_t(2) * sms * S::kWarps * floats * 4);
+  const size_t joined = parts + align256(size_t(sms) * S::kWarps * floats * 4);
   if (sc) *sc = Scratch{reinterpret_cast<float*>(base + parts), reinterpret_cast<float*>(base + joined),
                         reinterpret_cast<Open*>(base + open), rows, floats};
   return joined + align256(size_t(2) * sms * floats * 4);
@@ -881,7 +946,7 @@ cudaError_t launch_shape(const AttendArgs& a, cudaStream_t stream, int sms) {
   if ((e = launch_pdl(kv_attend_kernel<D, NR>, dim3(sms), dim3(S::kThreads), S::kSmem, stream, a, mk, mv, sc, limit, wait)) !=
       cudaSuccess)
     return e;
-  e = launch_pdl(kv_join_kernel<D, NR>, dim3(sms), dim3(kJoinWarps * 32), 0, stream, a, sc);
+  e = launch_pdl(kv_join_kernel<D>, dim3(sms, sc.rows), dim3(kJoinWarps * 32), 0, stream, a, sc);
   if (e != cudaSuccess || rows <= limit) return e;
   e = cudaFuncSetAttribute(kv_attend_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
