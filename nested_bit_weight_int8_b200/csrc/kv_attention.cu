@@ -882,40 +882,24 @@ kv_join_kernel(const AttendArgs a, const Scratch sc) {
   write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
 }
 
-// Sequences with more than `limit` rows (prompts): a warp per item, unsplit.
-template <int D, int NR>
-__global__ void __launch_bounds__(Shape<D, NR>::kThreads, 1)
-kv_attend_rows_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                      int limit, int row_tiles_max, uint64_t wait_ns) {
-  using S = Shape<D, NR>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kWarps = S::kWarps;
-  __shared__ uint64_t s_full[kWarps][S::kStages];
-  __shared__ float2 s_scales[kWarps][S::kStages * S::kGroups];
-  if (threadIdx.x < kWarps * S::kStages) mbar_init(&s_full[0][0] + threadIdx.x, S::kGroups);
-  fence_mbar_init();
-  __syncthreads();
-  pdl_launch_dependents();
-  pdl_wait_primary();
-  const int warp = threadIdx.x >> 5;
-  const int s = blockIdx.z, h = blockIdx.y;
-  const Seq sq = load_seq(a.b, s, nullptr);
-  const int rt = row_tiles_max - 1 - (blockIdx.x * kWarps + warp);  // long rows first
-  if (sq.n * a.group <= limit || rt < 0 || rt >= row_tiles<S::kRows>(a, sq)) return;
-  const RowTile it = row_tile<S::kRows, S::kTile, S::kStart>(a, sq, rt);
-  Ring<D, NR> ring{((smem_u32(smem) + 1023u) & ~1023u) + warp * S::kWarpBytes, s_full[warp], s_scales[warp], &map_k, &map_v,
-                   wait_ns, 0, 0};
-  Worker<D, NR>::run(a, sq, s, h, rt, 0, it.tiles, nullptr, 0, ring);
-}
-
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // Rows a tile, in eights: the fewest that take all of a sequence's rows, up to
 // what the accumulators leave room for.
 int row_eights(int D, int64_t rows) { return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4; }
-// Sequences with more rows than this go to the kernel for prompts.
-int row_limit(int D) { return D == 256 ? 64 : 128; }
+// Which kernel serves which sequences: up to `limit` rows here, `eights` a tile,
+// more in the kernel for prompts. A call whose sequences all have few rows splits
+// them here; where some have many, this kernel keeps those with single tokens.
+struct Share {
+  int eights, limit;
+};
+Share share_of(int D, int64_t max_new, int group) {
+  const int64_t rows = max_new * group, few = D == 256 ? 64 : 128;
+  if (rows <= few) return Share{row_eights(D, rows), static_cast<int>(few)};
+  const int e = row_eights(D, group);
+  return Share{e, 8 * e > group ? 8 * e : group};
+}
 
 template <int D, int NR>
 size_t scratch_shape(const KvCache& c, const KvBatch& b, int group, int sms, Scratch* sc = nullptr, uint8_t* base = nullptr) {
@@ -929,7 +913,7 @@ size_t scratch_shape(const KvCache& c, const KvBatch& b, int group, int sms, Scr
 }
 
 template <int D, int NR>
-cudaError_t launch_shape(const AttendArgs& a, cudaStream_t stream, int sms) {
+cudaError_t launch_shape(const AttendArgs& a, int limit, cudaStream_t stream, int sms) {
   using S = Shape<D, NR>;
   CUtensorMap mk, mv;
   const uint64_t rows_page = uint64_t(a.c.heads) * a.c.page;
@@ -940,25 +924,19 @@ cudaError_t launch_shape(const AttendArgs& a, cudaStream_t stream, int sms) {
     return e;
   Scratch sc;
   scratch_shape<D, NR>(a.c, a.b, a.group, sms, &sc, a.scratch);
-  const int limit = row_limit(D);
   const int64_t rows = int64_t(a.b.max_new) * a.group;
   const uint64_t wait = wait_limit_ns();
   if ((e = launch_pdl(kv_attend_kernel<D, NR>, dim3(sms), dim3(S::kThreads), S::kSmem, stream, a, mk, mv, sc, limit, wait)) !=
       cudaSuccess)
     return e;
   e = launch_pdl(kv_join_kernel<D>, dim3(sms, sc.rows), dim3(kJoinWarps * 32), 0, stream, a, sc);
-  if (e != cudaSuccess || rows <= limit) return e;
-  e = cudaFuncSetAttribute(kv_attend_rows_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
-  const int all = static_cast<int>((rows + S::kRows - 1) / S::kRows);
-  return launch_pdl(kv_attend_rows_kernel<D, NR>, dim3((all + S::kWarps - 1) / S::kWarps, a.c.heads, a.b.n_seqs),
-                    dim3(S::kThreads), S::kSmem, stream, a, mk, mv, limit, all, wait);
+  return e != cudaSuccess || rows <= limit ? e : launch_kv_prompt(a, limit, stream);
 }
 
 }  // namespace
 
 size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms) {
-  const int D = padded(c.d), n = row_eights(D, int64_t(b.max_new) * group);
+  const int D = padded(c.d), n = share_of(D, b.max_new, group).eights;
   if (D == 64) return n == 1 ? scratch_shape<64, 1>(c, b, group, sms) : n == 2 ? scratch_shape<64, 2>(c, b, group, sms)
                                                                               : scratch_shape<64, 4>(c, b, group, sms);
   if (D == 128) return n == 1 ? scratch_shape<128, 1>(c, b, group, sms) : n == 2 ? scratch_shape<128, 2>(c, b, group, sms)
@@ -967,12 +945,14 @@ size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int s
 }
 
 cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms) {
-  const int D = padded(a.c.d), n = row_eights(D, int64_t(a.b.max_new) * a.group);
-  if (D == 64) return n == 1 ? launch_shape<64, 1>(a, stream, sms) : n == 2 ? launch_shape<64, 2>(a, stream, sms)
-                                                                           : launch_shape<64, 4>(a, stream, sms);
-  if (D == 128) return n == 1 ? launch_shape<128, 1>(a, stream, sms) : n == 2 ? launch_shape<128, 2>(a, stream, sms)
-                                                                             : launch_shape<128, 4>(a, stream, sms);
-  return n == 1 ? launch_shape<256, 1>(a, stream, sms) : launch_shape<256, 2>(a, stream, sms);
+  const int D = padded(a.c.d);
+  const Share sh = share_of(D, a.b.max_new, a.group);
+  const int n = sh.eights, limit = sh.limit;
+  if (D == 64) return n == 1 ? launch_shape<64, 1>(a, limit, stream, sms) : n == 2 ? launch_shape<64, 2>(a, limit, stream, sms)
+                                                                                  : launch_shape<64, 4>(a, limit, stream, sms);
+  if (D == 128) return n == 1 ? launch_shape<128, 1>(a, limit, stream, sms) : n == 2 ? launch_shape<128, 2>(a, limit, stream, sms)
+                                                                                    : launch_shape<128, 4>(a, limit, stream, sms);
+  return n == 1 ? launch_shape<256, 1>(a, limit, stream, sms) : launch_shape<256, 2>(a, limit, stream, sms);
 }
 
 }  // namespace mq

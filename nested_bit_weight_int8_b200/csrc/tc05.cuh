@@ -45,6 +45,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
 // Arrives once on the mbarrier when every tcgen05 operation this thread
 // issued before has completed.
 __device__ __forceinline__ void commit(uint32_t mbar_smem) {
@@ -94,6 +104,16 @@ __device__ __forceinline__ void ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[32])
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -111,6 +131,21 @@ __device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t smem_addr) {
   d |= static_cast<uint64_t>(1u) << 46;                            // version (sm_100)
   d |= static_cast<uint64_t>(2u) << 61;                            // 128-byte swizzle
   return d;
+}
+
+// The same atoms with the operand's long side (64 values of it) along the 128
+// bytes and 8 steps of K on the rows: `block` bytes between blocks of 64 values,
+// 1024 between 8 steps of K. Goes with bit 16 of the instruction descriptor (B).
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint32_t block) {
+  return (desc_kmajor_sw128(smem_addr) & ~(uint64_t(0x3FFF) << 16)) | static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16;
+}
+
+// Instruction descriptor of kind::f16 with fp16 A and B (A K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4)                                   // D format: f32 (A and B formats 0: f16)
+         | (b_mn_major ? 1u << 16 : 0u)
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, both

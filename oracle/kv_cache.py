@@ -84,10 +84,11 @@ def out_error(out: np.ndarray, mass: np.ndarray, gross: np.ndarray, unit: float,
     scale of the value's page. Probabilities below 2^-22 of the running maximum,
     which is at most the largest, are fp16 subnormals: half a step there is 2^-25 of
     the factor 2^-8 they stand high, 2^-33 of the largest, a token each, times its
-    code and `unit`, the largest scale of V (which their ratio was taken to)."""
+    code and twice `unit`, the largest scale of V (their ratio is taken to it, or to
+    the power of two above it)."""
     u = 2.0 ** -24
     rel = 2 * np.expm1(delta)[:, None] + 2.0 ** -20 + 2.0 ** -11
-    under = tokens * 2.0 ** -33 * 127 * unit
+    under = tokens * 2.0 ** -33 * 127 * 2 * unit
     return (2.0 ** -8 * np.abs(out) + rel * mass + 8 * u * (tokens / 16 + 32) * gross[:, None] + under) * (1 + 2.0 ** -8)
 
 
