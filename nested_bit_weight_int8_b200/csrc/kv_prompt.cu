@@ -39,7 +39,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 6.f;          // base 2
 constexpr float kPLog2 = 8.f;          // p' stands 2^8 high
 constexpr float kTinyScale = 0x1p-100f;  // V scales below this count as this
 
@@ -63,20 +62,41 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ void fma2(float& x, float& y, float f, float c) {
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 d, {%3, %3};\n\t"
-      "fma.rn.f32x2 a, a, b, d;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(f), "f"(c));
+// Pairs of fp32 in one 64-bit register.
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
 }
-__device__ __forceinline__ void add2(float& x, float& y, float u, float v) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(u), "f"(v));
+__device__ __forceinline__ uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Moves registers between the CTA's warpgroups: all four warps of one execute it.
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// True in one lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -90,7 +110,10 @@ struct Plan {
   static constexpr int kT = D == 256 ? 64 : 128;
   static constexpr int kSoft = 4 * kMt;
   static constexpr int kConv = D == 256 ? 8 : 4;
-  static constexpr int kThreads = 32 * (kSoft + kConv + 1);
+  static constexpr int kThreads = 512;  // the last four warps: one issues the products
+  // Registers of a softmax, a spreading and a product thread; the launch gives 128.
+  static constexpr int kSoftRegs = D == 256 ? 208 : 160, kConvRegs = 112, kMmaRegs = 80;
+  static_assert(kSoft * kSoftRegs + kConv * kConvRegs + 4 * kMmaRegs <= kThreads / 32 * 128, "the split fits the launch's registers");
   static constexpr int kRows = 128 * kMt;
   static constexpr int kGroups = kT / 16;
   static constexpr int kBlocks = D / 64;         // 64 values of each row side by side
@@ -128,7 +151,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   volatile int* s_abort = &s_abort_word;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq_base = base, sk_base = base + P::kQBytes, sv_base = sk_base + 2 * P::kKvBytes;
 
@@ -186,6 +209,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
 
   if (warp < P::kSoft) {
     // ------------------------------------------------------------ softmax
+    more_registers<P::kSoftRegs>();
     const int mt = warp >> 2, r = 32 * (warp & 3) + lane, lr = 128 * mt + r;
     const bool live = lr < rows;
     const int row = row0 + lr, qi = row / a.group, hq = h * a.group + row - qi * a.group;
@@ -236,109 +260,141 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       const int jt = j0 + i * kT;
       const bool special =
           a.softcap > 0.f || ts.dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window) || row0 + 128 * mt + 128 > all_rows;
-      uint32_t pk[kT / 2];
-      float top, sum;
-      // Scores of one 16-token group: scaled, capped and masked where needed; f is then their factor.
-      auto group_scores = [&](float (&x)[16], int g, float& f) {
+      // Scores of one 16-token group, capped and masked where needed; f: their factor.
+      auto masked_scores = [&](float (&x)[16], int g, float& f) {
         const float4 sg = ts.group[g];
         f = fac * sg.x;
-        if (special) {
+        if (!special) return;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y = x[e] * f;
-            if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
-            const int j = jt + 16 * g + e;
-            x[e] = j > place || (a.window > 0 && j <= place - a.window) || sg.w == 0.f ? -INFINITY : y;
-          }
-          f = 1.f;
+        for (int e = 0; e < 16; ++e) {
+          float y = x[e] * f;
+          if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
+          const int j = jt + 16 * g + e;
+          x[e] = j > place || (a.window > 0 && j <= place - a.window) || sg.w == 0.f ? -INFINITY : y;
         }
-        float t = x[0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) t = fmaxf(t, x[e]);
-        top = fmaxf(top, t * f);
+        f = 1.f;
       };
-      auto maxima = [&]() {
-        top = -INFINITY;
+      auto largest = [&](int g0, int g1) {  // score of groups g0 .. g1 - 1
+        float top = -INFINITY;
 #pragma unroll 1
-        for (int g = 0; g < P::kGroups; ++g) {
+        for (int g = g0; g < g1; ++g) {
           uint32_t v[16];
           tc05::ld_32x32b_x16(t_s + 16 * g, v);
           tc05::wait_ld();
           float x[16], f;
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
-          group_scores(x, g, f);
+          masked_scores(x, g, f);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e] * f);
         }
+        return top;
       };
-      auto weights = [&](float m0) {
-        top = -INFINITY;
-        sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < kT / 32; ++c) {
-          uint32_t v[32];
-          tc05::ld_32x32b_x32(t_s + 32 * c, v);
-          tc05::wait_ld();
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int g = 2 * c + half;
-            float x[16], f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[16 * half + e]);
-            group_scores(x, g, f);
-            const float add = ts.group[g].y - m0;
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              fma2(x[e], x[e + 1], f, add);
-              const float p0 = exp2_fast(x[e]), p1 = exp2_fast(x[e + 1]);
-              add2(s0, s1, p0, p1);
-              pk[8 * g + e / 2] = f16x2(p0, p1);
-            }
-            sum = fmaf(s0 + s1, ts.group[g].z, sum);
-          }
-        }
-      };
-      // Raises the maximum to this tile's and the V scale to the tile's, and O with them.
-      auto raise = [&]() -> bool {
-        const float x = fmaxf(top, m);
-        const float k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / ts.vmax);
+      // Raises the maximum (an integer, so that the factors are powers of two) to
+      // `top` and the V scale to the tile's; O, and the first `done` columns of P, follow.
+      float sum = 0.f;
+      auto raise = [&](float top, int done) -> bool {
+        const float x = fmaxf(ceilf(top), m), k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / ts.vmax);
         l *= k;
+        sum *= k;
         m = x;
         vmax = ts.vmax;
-        if (i == 0) return true;
-        if (!wait(&bar.o_done[mt], (i - 1) & 1, kErrMma)) return false;
-        tc05::fence_after_sync();
+        const __half2 k2 = __float2half2_rn(k);
+        tc05::wait_st();  // P so far
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[32];
-          tc05::ld_32x32b_x32(t_o + 32 * c, v);
+        for (int c = 0; c < done; c += 16) {
+          uint32_t v[16];
+          tc05::ld_32x32b_x16(t_s + c, v);
           tc05::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
-          tc05::st_32x32b_x32(t_o + 32 * c, v);
+          for (int e = 0; e < 16; ++e) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), k2);
+            v[e] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          tc05::st_32x32b_x16(t_s + c, v);
+        }
+        if (i > 0) {
+          if (!wait(&bar.o_done[mt], (i - 1) & 1, kErrMma)) return false;
+          tc05::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tc05::ld_32x32b_x16(t_o + 16 * c, v);
+            tc05::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
+            tc05::st_32x32b_x16(t_o + 16 * c, v);
+          }
         }
         tc05::wait_st();
         return true;
       };
-      if (i == 0) {
-        maxima();
-        raise();
+      // rows that have seen nothing yet take this tile's maximum first
+      const bool fresh = __any_sync(0xffffffffu, live && m == -INFINITY);
+      if (fresh || ts.vmax != vmax) {
+        if (!(ok = raise(fresh ? largest(0, P::kGroups) : -INFINITY, 0))) break;
       }
-      // with the maximum so far; done over where a score passes it by the slack
-      while (true) {
-        weights(m == -INFINITY ? 0.f : m);
-        if (!__any_sync(0xffffffffu, top > m + kSlack || ts.vmax != vmax)) break;
-        if (!(ok = raise())) break;
+      // 32 tokens: p' to fp16, over scores that are read already. The running maximum
+      // is not looked for: a score that passes it by more than 6 or so shows in the sum.
+      auto weights = [&](const uint32_t (&v)[32], int c) -> bool {
+        uint32_t pk[16];
+        while (true) {
+          const float m0 = m == -INFINITY ? 0.f : m;
+          float part = 0.f, big = 0.f;
+          auto group = [&](auto score, float f, int half) {
+            const float4 sg = ts.group[2 * c + half];
+            const uint64_t f2 = pair(f, f), c2 = pair(sg.y - m0, sg.y - m0);
+            uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float2 x = unpair(fma2(score(e), f2, c2)), y = unpair(fma2(score(e + 2), f2, c2));
+              const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
+              s0 = add2(s0, pair(p0, p1));
+              s1 = add2(s1, pair(p2, p3));
+              pk[8 * half + e / 2] = f16x2(p0, p1);
+              pk[8 * half + e / 2 + 1] = f16x2(p2, p3);
+            }
+            const float2 t = unpair(add2(s0, s1));
+            big = fmaxf(big, t.x + t.y);
+            part = fmaf(t.x + t.y, sg.z, part);
+          };
+          if (!special) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              group([&](int e) { return pair(v[16 * half + e], v[16 * half + e + 1]); }, fac * ts.group[2 * c + half].x, half);
+          } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float x[16], f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[16 * half + e]);
+              masked_scores(x, 2 * c + half, f);
+              group([&](int e) { return pair(x[e], x[e + 1]); }, f, half);
+            }
+          }
+          if (!__any_sync(0xffffffffu, big > 32768.f)) {
+            sum += part;
+            break;
+          }
+          tc05::wait_ld();  // the next scores, on their way
+          if (!raise(largest(2 * c, 2 * c + 2), 16 * c)) return false;
+        }
+        tc05::st_32x32b_x16(t_s + 16 * c, pk);
+        return true;
+      };
+      uint32_t va[32], vb[32];
+      tc05::ld_32x32b_x32(t_s, va);
+#pragma unroll 1
+      for (int c = 0; c < kT / 32; c += 2) {
+        tc05::wait_ld();
+        tc05::ld_32x32b_x32(t_s + 32 * (c + 1), vb);
+        if (!(ok = weights(va, c))) break;
+        tc05::wait_ld();
+        if (c + 2 < kT / 32) tc05::ld_32x32b_x32(t_s + 32 * (c + 2), va);
+        if (!(ok = weights(vb, c + 1))) break;
       }
       if (!ok) break;
       l += sum;
-#pragma unroll
-      for (int c = 0; c < kT / 64; ++c) {
-        uint32_t v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = pk[32 * c + e];
-        tc05::st_32x32b_x32(t_s + 32 * c, v);
-      }
       tc05::wait_st();
       tc05::fence_before_sync();
       __syncwarp();
@@ -373,6 +429,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     }
   } else if (warp < P::kSoft + P::kConv) {
     // ------------------------------------------------------------ bytes to fp16
+    fewer_registers<P::kConvRegs>();
     const int cw = warp - P::kSoft;
     constexpr int kTokens = kT / P::kConv;       // of this warp
     constexpr int kWide = D / 64;                // a row's chunks in fours
@@ -385,7 +442,14 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     // lane g < kGroups: the page of group g of a tile
     auto page_of = [&](int i) {
       const int j = j0 + i * kT + 16 * lane;
-      return lane < P::kGroups && j < j1 && j + 16 > lo ? load_page(a.c, a.b, s, j >> log2p, a.err) : -1;
+      return lane < P::kGroups && j < j1 && j + 16 > lo ? a.b.pages[int64_t(s) * a.b.max_pages + (j >> log2p)] : -1;
+    };
+    // checked where it is used, so that the load runs ahead
+    auto checked = [&](int pid, int i) {
+      const int j = j0 + i * kT + 16 * lane;
+      if (pid >= 0 && pid < a.c.n_pages) return pid;
+      if (lane < P::kGroups && j < j1 && j + 16 > lo) atomicOr(a.err, kErrBounds);
+      return -1;
     };
     uint4 xk[kIt], xv[kIt];
     float2 sc = make_float2(0.f, 0.f);  // lane's group: K, V scale
@@ -419,7 +483,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       __syncwarp();
     };
     float vmax = kTinyScale;
-    int pid = n > 0 ? page_of(0) : -1;
+    int pid = n > 0 ? checked(page_of(0), 0) : -1;
     if (n > 0) fetch(0, pid);
     int next = n > 1 ? page_of(1) : -1;
     for (int i = 0; i < n; ++i) {
@@ -450,35 +514,45 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       spread(sv_base + b * P::kKvBytes, xv);
       if (lane == 0) mbar_arrive(&bar.v_full[b]);
       if (i + 1 < n) {
-        pid = next;
+        pid = checked(next, i + 1);
         fetch(i + 1, pid);
         if (i + 2 < n) next = page_of(i + 2);
       }
     }
-  } else if (lane == 0 && n > 0) {
+  } else {
     // ------------------------------------------------------------ products
-    auto wait1 = [&](uint64_t* b, uint32_t parity) {
-      if (*s_abort == 0 && mbar_wait_bounded(b, parity, wait_ns)) return true;
-      atomicOr(a.err, kErrMma);
-      *s_abort = 1;
-      return false;
+    fewer_registers<P::kMmaRegs>();
+    // The whole warp walks the loop, so that descriptors stay in uniform registers
+    // (a lone thread's moves to them cost more than the products); one lane issues.
+    if (warp == P::kSoft + P::kConv && n > 0) {
+    const bool leader = elect_one();
+    auto wait1 = [&](uint64_t* b, uint32_t parity) { return wait(b, parity, kErrMma); };
+    auto commit = [&](uint64_t* b) {
+      if (leader) tc05::commit(smem_u32(b));
     };
     constexpr uint32_t id_s = tc05::idesc_f16_f32(128, kT, false), id_o = tc05::idesc_f16_f32(128, D, true);
+    // One thread issues every product: their descriptors are sums of a base and constants (16-byte units).
+    const uint64_t desc_q = tc05::desc_kmajor_sw128(sq_base), desc_k = tc05::desc_kmajor_sw128(sk_base);
+    const uint64_t desc_v = tc05::desc_mnmajor_sw128(sv_base, P::kBlocks > 1 ? P::kKvBlock : 1024);
     auto scores = [&](int mt, int slot, int i) {  // S = Q K^T of tile i
-      const uint32_t kb = sk_base + (i & 1) * P::kKvBytes, qb = sq_base + mt * P::kBlocks * P::kQBlock;
+      const uint64_t q = desc_q + mt * (P::kBlocks * P::kQBlock >> 4), k0 = desc_k + (i & 1) * (P::kKvBytes >> 4);
+      const uint32_t to = tmem + slot * kT;
+      if (leader) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc05::mma_ss(tmem + slot * kT, tc05::desc_kmajor_sw128(qb + (k >> 2) * P::kQBlock + (k & 3) * 32),
-                     tc05::desc_kmajor_sw128(kb + (k >> 2) * P::kKvBlock + (k & 3) * 32), id_s, k > 0);
-      tc05::commit(smem_u32(&bar.s_full[slot]));
+        for (int k = 0; k < D / 16; ++k)
+          tc05::mma_ss(to, q + (((k >> 2) * P::kQBlock + (k & 3) * 32) >> 4), k0 + (((k >> 2) * P::kKvBlock + (k & 3) * 32) >> 4),
+                       id_s, k > 0);
+        tc05::commit(smem_u32(&bar.s_full[slot]));
+      }
     };
     auto outputs = [&](int mt, int slot, int i) {  // O += P V of tile i
-      const uint32_t vb = sv_base + (i & 1) * P::kKvBytes;
+      const uint64_t v0 = desc_v + (i & 1) * (P::kKvBytes >> 4);
+      const uint32_t to = tmem + P::kOCol + mt * D, p = tmem + slot * kT;
+      if (leader) {
 #pragma unroll
-      for (int k = 0; k < kT / 16; ++k)
-        tc05::mma_ts(tmem + P::kOCol + mt * D, tmem + slot * kT + 8 * k, tc05::desc_mnmajor_sw128(vb + k * 2048, P::kBlocks > 1 ? P::kKvBlock : 1024), id_o,
-                     i > 0 || k > 0);
-      tc05::commit(smem_u32(&bar.o_done[mt]));
+        for (int k = 0; k < kT / 16; ++k) tc05::mma_ts(to, p + 8 * k, v0 + (k * 2048 >> 4), id_o, i > 0 || k > 0);
+        tc05::commit(smem_u32(&bar.o_done[mt]));
+      }
     };
     auto full = [&](uint64_t (&b)[2], int i) {
       if (!wait1(&b[i & 1], (i >> 1) & 1)) return false;
@@ -491,7 +565,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       if (ok) {
         scores(0, 0, 0);
         scores(1, 1, 0);
-        tc05::commit(smem_u32(&bar.k_empty[0]));
+        commit(&bar.k_empty[0]);
       }
       for (int i = 0; ok && i < n; ++i) {
 #pragma unroll
@@ -500,11 +574,11 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
           if (!(ok = wait1(&bar.p_full[mt], i & 1))) break;
           tc05::fence_after_sync();
           outputs(mt, mt, i);
-          if (mt == 1) tc05::commit(smem_u32(&bar.v_empty[i & 1]));
+          if (mt == 1) commit(&bar.v_empty[i & 1]);
           if (i + 1 < n) {
             if (mt == 0 && !(ok = full(bar.k_full, i + 1))) break;
             scores(mt, mt, i + 1);
-            if (mt == 1) tc05::commit(smem_u32(&bar.k_empty[(i + 1) & 1]));
+            if (mt == 1) commit(&bar.k_empty[(i + 1) & 1]);
           }
         }
       }
@@ -512,23 +586,24 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       for (int i = 0; ok && i < 2 && i < n; ++i) {
         if (!(ok = full(bar.k_full, i))) break;
         scores(0, i, i);
-        tc05::commit(smem_u32(&bar.k_empty[i]));
+        commit(&bar.k_empty[i]);
       }
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = full(bar.v_full, i) && wait1(&bar.p_full[i & 1], (i >> 1) & 1))) break;
         tc05::fence_after_sync();
         outputs(0, i & 1, i);
-        tc05::commit(smem_u32(&bar.v_empty[i & 1]));
+        commit(&bar.v_empty[i & 1]);
         if (i + 2 < n) {
           if (!(ok = full(bar.k_full, i + 2))) break;
           scores(0, i & 1, i + 2);
-          tc05::commit(smem_u32(&bar.k_empty[i & 1]));
+          commit(&bar.k_empty[i & 1]);
         }
       }
     }
     // all products that this thread issued have finished before the CTA moves on
-    tc05::commit(smem_u32(&bar.drain));
-    if (!mbar_wait_bounded(&bar.drain, 0, 1000000000ull)) atomicOr(a.err, kErrDrain);
+    commit(&bar.drain);
+    if (!mbar_wait_bounded(&bar.drain, 0, 1000000000ull) && leader) atomicOr(a.err, kErrDrain);
+    }
   }
   __syncthreads();
   if (warp == P::kSoft + P::kConv) {
