@@ -112,7 +112,7 @@ struct Plan {
   static constexpr int kConv = D == 256 ? 8 : 4;
   static constexpr int kThreads = 512;  // the last four warps: one issues the products
   // Registers of a softmax, a spreading and a product thread; the launch gives 128.
-  static constexpr int kSoftRegs = D == 256 ? 208 : 160, kConvRegs = 112, kMmaRegs = 80;
+  static constexpr int kSoftRegs = D == 256 ? 208 : 168, kConvRegs = 112, kMmaRegs = 64;
   static_assert(kSoft * kSoftRegs + kConv * kConvRegs + 4 * kMmaRegs <= kThreads / 32 * 128, "the split fits the launch's registers");
   static constexpr int kRows = 128 * kMt;
   static constexpr int kGroups = kT / 16;
@@ -217,27 +217,41 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     const int place = live ? past + qi : -1;
     float fac;
     {  // this thread's query, scaled by a power of two to below 2
-      const uint16_t* qp = a.q + grow * a.q_stride + int64_t(hq) * d;
-      float mx = 0.f;
-      for (int c = 0; c < 2 * chunks; ++c) {
-        const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(qp) + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint4* qp = reinterpret_cast<const uint4*>(a.q + grow * a.q_stride + int64_t(hq) * d);
+      constexpr int kAll = D / 8, kBatch = kAll < 16 ? kAll : 16;  // loads on their way at once
+      uint4 u[kBatch];
+      auto load = [&](int c0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        for (int c = 0; c < kBatch; ++c) u[c] = live && c0 + c < 2 * chunks ? __ldg(qp + c0 + c) : make_uint4(0, 0, 0, 0);
+      };
+      float mx = 0.f;
+#pragma unroll
+      for (int c0 = kAll - kBatch; c0 >= 0; c0 -= kBatch) {
+        load(c0);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        }
       }
       int ex = __float_as_int(mx) >> 23;
       ex = ex < 1 || ex > 253 ? 127 : ex;
       const float down = __int_as_float((254 - ex) << 23) * (a.scale < 0.f ? -1.f : 1.f);
       fac = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
-#pragma unroll 4
-      for (int c = 0; c < 8 * P::kBlocks; ++c) {
-        const uint4 u = live && c < 2 * chunks ? __ldg(reinterpret_cast<const uint4*>(qp) + c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-        sts128(sq_base + (mt * P::kBlocks + (c >> 3)) * P::kQBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+      for (int c0 = 0; c0 < kAll; c0 += kBatch) {
+        if (c0 > 0) load(c0);
+#pragma unroll
+        for (int c = 0; c < kBatch; ++c) {
+          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+          uint32_t x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
+          const int at = c0 + c;
+          sts128(sq_base + (mt * P::kBlocks + (at >> 3)) * P::kQBlock + r * 128 + (((at & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+        }
       }
       fence_async_smem();
       __syncwarp();
@@ -274,10 +288,10 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
         }
         f = 1.f;
       };
-      auto largest = [&](int g0, int g1) {  // score of groups g0 .. g1 - 1
+      auto largest = [&]() {  // score of the tile
         float top = -INFINITY;
 #pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
+        for (int g = 0; g < P::kGroups; ++g) {
           uint32_t v[16];
           tc05::ld_32x32b_x16(t_s + 16 * g, v);
           tc05::wait_ld();
@@ -291,40 +305,23 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
         return top;
       };
       // Raises the maximum (an integer, so that the factors are powers of two) to
-      // `top` and the V scale to the tile's; O, and the first `done` columns of P, follow.
-      float sum = 0.f;
-      auto raise = [&](float top, int done) -> bool {
+      // `top` and the V scale to the tile's; O follows.
+      auto raise = [&](float top) -> bool {
         const float x = fmaxf(ceilf(top), m), k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / ts.vmax);
         l *= k;
-        sum *= k;
         m = x;
         vmax = ts.vmax;
-        const __half2 k2 = __float2half2_rn(k);
-        tc05::wait_st();  // P so far
+        if (i == 0) return true;
+        if (!wait(&bar.o_done[mt], (i - 1) & 1, kErrMma)) return false;
+        tc05::fence_after_sync();
 #pragma unroll 1
-        for (int c = 0; c < done; c += 16) {
+        for (int c = 0; c < D / 16; ++c) {
           uint32_t v[16];
-          tc05::ld_32x32b_x16(t_s + c, v);
+          tc05::ld_32x32b_x16(t_o + 16 * c, v);
           tc05::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), k2);
-            v[e] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          tc05::st_32x32b_x16(t_s + c, v);
-        }
-        if (i > 0) {
-          if (!wait(&bar.o_done[mt], (i - 1) & 1, kErrMma)) return false;
-          tc05::fence_after_sync();
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t v[16];
-            tc05::ld_32x32b_x16(t_o + 16 * c, v);
-            tc05::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
-            tc05::st_32x32b_x16(t_o + 16 * c, v);
-          }
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
+          tc05::st_32x32b_x16(t_o + 16 * c, v);
         }
         tc05::wait_st();
         return true;
@@ -332,69 +329,71 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       // rows that have seen nothing yet take this tile's maximum first
       const bool fresh = __any_sync(0xffffffffu, live && m == -INFINITY);
       if (fresh || ts.vmax != vmax) {
-        if (!(ok = raise(fresh ? largest(0, P::kGroups) : -INFINITY, 0))) break;
+        if (!(ok = raise(fresh ? largest() : -INFINITY))) break;
       }
-      // 32 tokens: p' to fp16, over scores that are read already. The running maximum
-      // is not looked for: a score that passes it by more than 6 or so shows in the sum.
-      auto weights = [&](const uint32_t (&v)[32], int c) -> bool {
-        uint32_t pk[16];
-        while (true) {
-          const float m0 = m == -INFINITY ? 0.f : m;
-          float part = 0.f, big = 0.f;
-          auto group = [&](auto score, float f, int half) {
-            const float4 sg = ts.group[2 * c + half];
-            const uint64_t f2 = pair(f, f), c2 = pair(sg.y - m0, sg.y - m0);
-            uint64_t s0 = 0, s1 = 0;
+      // p' of the whole tile, in registers: no branch between its scores, so that their
+      // loads, exponentials and sums overlap. The running maximum is not looked for: a
+      // score that passes it by more than 6 or so shows in its group's sum, and the
+      // tile is done over.
+      uint32_t pk[kT / 2];
+      float sum, big;
+      auto group = [&](auto score, float f, int g, float m0) {
+        const float4 sg = ts.group[g];
+        const uint64_t f2 = pair(f, f), c2 = pair(sg.y - m0, sg.y - m0);
+        uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float2 x = unpair(fma2(score(e), f2, c2)), y = unpair(fma2(score(e + 2), f2, c2));
-              const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
-              s0 = add2(s0, pair(p0, p1));
-              s1 = add2(s1, pair(p2, p3));
-              pk[8 * half + e / 2] = f16x2(p0, p1);
-              pk[8 * half + e / 2 + 1] = f16x2(p2, p3);
-            }
-            const float2 t = unpair(add2(s0, s1));
-            big = fmaxf(big, t.x + t.y);
-            part = fmaf(t.x + t.y, sg.z, part);
-          };
-          if (!special) {
+        for (int e = 0; e < 16; e += 4) {
+          const float2 x = unpair(fma2(score(e), f2, c2)), y = unpair(fma2(score(e + 2), f2, c2));
+          const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
+          s0 = add2(s0, pair(p0, p1));
+          s1 = add2(s1, pair(p2, p3));
+          pk[8 * g + e / 2] = f16x2(p0, p1);
+          pk[8 * g + e / 2 + 1] = f16x2(p2, p3);
+        }
+        const float2 t = unpair(add2(s0, s1));
+        big = fmaxf(big, t.x + t.y);
+        sum = fmaf(t.x + t.y, sg.z, sum);
+      };
+      while (true) {
+        const float m0 = m == -INFINITY ? 0.f : m;
+        sum = big = 0.f;
+        if (!special) {
+          uint32_t v[2][32];
+          tc05::ld_32x32b_x32(t_s, v[0]);
+#pragma unroll
+          for (int c = 0; c < kT / 32; ++c) {
+            tc05::wait_ld();
+            if (c + 1 < kT / 32) tc05::ld_32x32b_x32(t_s + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-              group([&](int e) { return pair(v[16 * half + e], v[16 * half + e + 1]); }, fac * ts.group[2 * c + half].x, half);
-          } else {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float x[16], f;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[16 * half + e]);
-              masked_scores(x, 2 * c + half, f);
-              group([&](int e) { return pair(x[e], x[e + 1]); }, f, half);
-            }
+              group([&](int e) { return pair(v[c & 1][16 * half + e], v[c & 1][16 * half + e + 1]); },
+                    fac * ts.group[2 * c + half].x, 2 * c + half, m0);
           }
-          if (!__any_sync(0xffffffffu, big > 32768.f)) {
-            sum += part;
-            break;
+        } else {
+#pragma unroll
+          for (int g = 0; g < P::kGroups; ++g) {
+            uint32_t v[16];
+            tc05::ld_32x32b_x16(t_s + 16 * g, v);
+            tc05::wait_ld();
+            float x[16], f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
+            masked_scores(x, g, f);
+            group([&](int e) { return pair(x[e], x[e + 1]); }, f, g, m0);
           }
-          tc05::wait_ld();  // the next scores, on their way
-          if (!raise(largest(2 * c, 2 * c + 2), 16 * c)) return false;
         }
-        tc05::st_32x32b_x16(t_s + 16 * c, pk);
-        return true;
-      };
-      uint32_t va[32], vb[32];
-      tc05::ld_32x32b_x32(t_s, va);
-#pragma unroll 1
-      for (int c = 0; c < kT / 32; c += 2) {
-        tc05::wait_ld();
-        tc05::ld_32x32b_x32(t_s + 32 * (c + 1), vb);
-        if (!(ok = weights(va, c))) break;
-        tc05::wait_ld();
-        if (c + 2 < kT / 32) tc05::ld_32x32b_x32(t_s + 32 * (c + 2), va);
-        if (!(ok = weights(vb, c + 1))) break;
+        if (!__any_sync(0xffffffffu, big > 32768.f)) break;
+        if (!(ok = raise(largest()))) break;
       }
       if (!ok) break;
       l += sum;
+#pragma unroll
+      for (int c = 0; c < kT / 64; ++c) {
+        uint32_t v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = pk[32 * c + e];
+        tc05::st_32x32b_x32(t_s + 32 * c, v);
+      }
       tc05::wait_st();
       tc05::fence_before_sync();
       __syncwarp();
@@ -406,22 +405,22 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       tc05::fence_after_sync();
       const float inv = l > 0.f ? vmax * 0x1p-8f / l : (l == 0.f ? 0.f : l);
       uint16_t* op = a.out + grow * a.out_stride + int64_t(hq) * d;
-#pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t v[16] = {};
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32] = {};
         if (n > 0) {
-          tc05::ld_32x32b_x16(t_o + 16 * c, v);
+          tc05::ld_32x32b_x32(t_o + 32 * c, v);
           tc05::wait_ld();
         }
-        if (live && c < chunks) {
-          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
             w[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          reinterpret_cast<uint4*>(op + 16 * c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(op + 16 * c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          if (live && 2 * c + k / 2 < chunks) *reinterpret_cast<uint4*>(op + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       if (a.lse && live) a.lse[grow * (a.c.heads * a.group) + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
