@@ -92,7 +92,9 @@ cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream);
 size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
 // Sequences with more than `limit` rows (query tokens times heads of a group).
-cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, cudaStream_t stream);
+// `scratch`: kv_prompt_scratch bytes.
+size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
+cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms);
 cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms);
 
 #ifdef __CUDACC__

@@ -2,9 +2,11 @@
 // (prompts), on the fifth-generation tensor cores. Mathematics and masks are
 // those of kv_attention.cu; here the products bound the time, not the bytes.
 //
-// A CTA takes kMt tiles of 128 rows (query tokens times the heads of a group) of
-// one sequence and key/value head, and walks the tokens that they see in tiles of
-// kT. Per tile and 128 rows: S = Q K^T (128 x kT, in tensor memory), softmax, P
+// An item is kMt tiles of 128 rows (query tokens times the heads of a group) of one
+// sequence and key/value head, with the tokens that they see in tiles of kT. The
+// tiles of all items together are cut into equal ranges, one per SM, so that few long
+// prompts fill the card and no SM waits for another's last item; a second kernel
+// joins the items that several SMs shared. Per tile and 128 rows: S = Q K^T (128 x kT, in tensor memory), softmax, P
 // written over S as fp16, O += P V (128 x D, in tensor memory).
 //   warps 0 .. 4 kMt - 1 : softmax, a thread a row: S from tensor memory, running
 //                          maximum and sum in registers, P back; queries at the
@@ -27,9 +29,11 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mq.h"
 #include "kv_internal.h"
+#include "kv_pieces.cuh"
 #include "mq_device.cuh"
 #include "mq_internal.h"
 #include "tc05.cuh"
@@ -37,25 +41,9 @@
 namespace mq {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPLog2 = 8.f;          // p' stands 2^8 high
 constexpr float kTinyScale = 0x1p-100f;  // V scales below this count as this
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float tanh_fast(float x) {
-  float r;  // 1 - 2 / (1 + e^2x): within 2^-22 absolutely, which is what a score needs
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(2.f * kLog2e * x)));
-  return fmaf(-2.f, r, 1.f);
-}
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // Two bytes of a word as the fp16 pair of byte - 128: 0x6400 | byte is 1024 + byte.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
   const uint32_t m = __byte_perm(w, 0x64646464u, sel);
@@ -83,6 +71,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// 2^x of two values on the multiply-add pipes, for x in [-126, 128): 2^round(x) times a
+// polynomial of degree 5 in the rest, |rest| <= 1/2, whose coefficients make the largest
+// relative error smallest (2^-23.7; 2^-22.2 in fp32). Below -126 it gives 2^-126.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x) {
+  const float2 v = unpair(x);
+  const uint64_t y = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  const uint64_t t = add2(y, pair(12582912.f, 12582912.f));  // 1.5 2^23: the integer in the low bits
+  const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), y);
+  uint64_t p = pair(0x1.5c08e6p-10f, 0x1.5c08e6p-10f);
+  p = fma2(p, f, pair(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+  p = fma2(p, f, pair(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
+  p = fma2(p, f, pair(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+  p = fma2(p, f, pair(0x1.62e428p-1f, 0x1.62e428p-1f));
+  p = fma2(p, f, pair(0x1.000002p+0f, 0x1.000002p+0f));
+  const float2 q = unpair(p), n = unpair(t);
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
 }
 // Moves registers between the CTA's warpgroups: all four warps of one execute it.
 template <int N>
@@ -125,6 +131,8 @@ struct Plan {
   static constexpr uint32_t kOCol = kMt * kT > 2 * kT ? kMt * kT : 2 * kT;  // behind the two S
   static_assert(kOCol + kMt * D <= 512, "S and O fit the tensor memory");
   static constexpr int kSlots = 4;  // scales: a tile's are read until its softmax ends
+  // What an item costs beside its tiles, in tiles: queries in, outputs out, the first bytes.
+  static constexpr int kStart = D == 256 ? 6 : 3;
 };
 
 struct TileScales {
@@ -140,38 +148,99 @@ struct Bars {
   uint64_t drain;
 };
 
+// An item's rows and tokens.
+struct Item {
+  int row0, rows;   // of the sequence
+  int past;         // place of the sequence's first row
+  int lo, j0, j1;   // first token that some row sees, rounded down to a tile, and their end
+  int n;            // tiles; 0 where no row sees a token
+  int start, units; // in the split: before the first tile, and in all
+};
+template <int D>
+__device__ __forceinline__ Item item_of(const AttendArgs& a, const Seq& sq, int rt) {
+  using P = Plan<D>;
+  Item t;
+  const int all = sq.n * a.group;
+  t.row0 = rt * P::kRows;
+  t.rows = min(P::kRows, all - t.row0);
+  t.past = sq.len - sq.n;
+  const int lo_place = t.past + t.row0 / a.group, hi_place = t.past + (t.row0 + t.rows - 1) / a.group;
+  t.j1 = max(hi_place + 1, 0);
+  t.lo = a.window > 0 ? max(lo_place - a.window + 1, 0) : 0;
+  t.j0 = t.lo & ~(P::kT - 1);
+  t.n = (t.j1 - t.j0 + P::kT - 1) / P::kT;
+  t.start = t.n > 0 ? P::kStart : 0;
+  t.units = t.n > 0 ? t.n + P::kStart : 1;
+  return t;
+}
+template <int D>
+__device__ __forceinline__ int item_rows(const AttendArgs& a, const Seq& sq, int limit) {
+  const int all = sq.n * a.group;
+  return all <= limit ? 0 : (all + Plan<D>::kRows - 1) / Plan<D>::kRows;
+}
+
+// A CTA's way through its range: sequences, their row tiles from the last, heads.
+struct Place {
+  int s, rt, h, u0;
+};
+template <int D>
+struct Walk {
+  Place at;
+  Seq sq;
+  Item it;
+  int64_t left;  // units of the range
+  int t0, t1;    // tiles of the piece
+  bool whole;
+  __device__ __forceinline__ void piece() {
+    const int u1 = static_cast<int>(min(int64_t(it.units), at.u0 + left));
+    t0 = max(at.u0 - it.start, 0);
+    t1 = max(u1 - it.start, 0);
+    if (it.n == 0) t0 = t1 = 0;
+    whole = t0 == 0 && t1 == it.n;
+  }
+  __device__ __forceinline__ bool empty() const { return it.n > 0 && t0 >= t1; }
+  __device__ __forceinline__ void start(const AttendArgs& a, const Place& p, int64_t units) {
+    at = p;
+    left = units;
+    sq = load_seq(a.b, at.s, nullptr);
+    it = item_of<D>(a, sq, at.rt);
+    piece();
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& a, int limit) {
+    left -= it.units - at.u0;
+    if (left <= 0) return false;
+    at.u0 = 0;
+    if (++at.h == a.c.heads) {
+      at.h = 0;
+      if (--at.rt < 0) {
+        do {
+          sq = load_seq(a.b, ++at.s, nullptr);
+          at.rt = item_rows<D>(a, sq, limit) - 1;
+        } while (at.rt < 0);
+      }
+      it = item_of<D>(a, sq, at.rt);
+    }
+    piece();
+    return true;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(Plan<D>::kThreads, 1)
-kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns) {
+kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait_ns) {
   using P = Plan<D>;
-  constexpr int kT = P::kT;
+  constexpr int kT = P::kT, kThreads = P::kThreads, kWarps = kThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bar;
   __shared__ TileScales s_scales[P::kSlots];
+  __shared__ int64_t s_pre[kThreads + 1], s_warp[kWarps];
+  __shared__ Place s_place;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   volatile int* s_abort = &s_abort_word;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq_base = base, sk_base = base + P::kQBytes, sv_base = sk_base + 2 * P::kKvBytes;
-
-  pdl_launch_dependents();
-  pdl_wait_primary();
-  // the longest rows first: tile index slowest, from the last
-  const int per_tile = a.c.heads * a.b.n_seqs;
-  const int rt = tiles_max - 1 - blockIdx.x / per_tile;
-  const int h = (blockIdx.x % per_tile) % a.c.heads, s = (blockIdx.x % per_tile) / a.c.heads;
-  const Seq sq = load_seq(a.b, s, nullptr);
-  const int all_rows = sq.n * a.group, row0 = rt * P::kRows;
-  if (all_rows <= limit || row0 >= all_rows) return;
-  const int rows = min(P::kRows, all_rows - row0);
-  const int past = sq.len - sq.n;  // place of the sequence's first row
-  const int lo_place = past + row0 / a.group, hi_place = past + (row0 + rows - 1) / a.group;
-  const int j1 = max(hi_place + 1, 0);
-  const int lo = a.window > 0 ? max(lo_place - a.window + 1, 0) : 0;
-  const int j0 = lo & ~(kT - 1);
-  const int n = (j1 - j0 + kT - 1) / kT;  // tiles; 0 where no row sees a token
-  const int d = a.c.d, chunks = d >> 4;
 
   if (tid == 0) {
     mbar_init(&bar.q_full, P::kSoft);
@@ -186,7 +255,85 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     }
     mbar_init(&bar.drain, 1);
     s_abort_word = 0;
+    s_pre[0] = 0;
     fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  // ---- units before each run of sequences: a warp sums a run
+  const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
+  auto seq_units = [&](int s) {  // of one sequence, by the warp
+    const Seq sq = load_seq(a.b, s, nullptr);
+    const int nrt = item_rows<D>(a, sq, limit);
+    int64_t units = 0;
+    for (int rt = lane; rt < nrt; rt += 32) units += item_of<D>(a, sq, rt).units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+    return units * a.c.heads;
+  };
+  s_pre[tid + 1] = 0;
+  __syncthreads();
+  for (int run = warp; run * per < a.b.n_seqs; run += kWarps) {
+    int64_t units = 0;
+    for (int s = run * per; s < min((run + 1) * per, a.b.n_seqs); ++s) units += seq_units(s);
+    if (lane == 0) s_pre[run + 1] = units;
+  }
+  __syncthreads();
+  int64_t inc = s_pre[tid + 1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int64_t sums = lane < kWarps ? s_warp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += up;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+  s_pre[tid + 1] = (warp == 0 ? 0 : __shfl_sync(0xffffffffu, sums, warp - 1)) + inc;
+  __syncthreads();
+  // ---- this CTA's range: a few tiles at least
+  const int cta = blockIdx.x;
+  const int ctas = static_cast<int>(min(int64_t(gridDim.x), max((total + P::kStart) / (P::kStart + 1), int64_t(1))));
+  if (tid == 0) scr.open[cta].rows = 0;
+  if (cta >= ctas || total == 0) return;
+  const Cut cut(total, ctas);
+  const int64_t A = cut.first(cta), B = cut.first(cta + 1);
+  if (warp == 0) {
+    int run = (__popc(__ballot_sync(0xffffffffu, s_pre[lane * kWarps] <= A)) - 1) * kWarps;
+    run += __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_pre[run + lane] <= A)) - 1;
+    int s = run * per;
+    int64_t off = A - s_pre[run];
+    while (true) {
+      const int64_t u = seq_units(s);
+      if (off < u) break;
+      off -= u;
+      ++s;
+    }
+    const Seq sq = load_seq(a.b, s, nullptr);
+    for (int first = item_rows<D>(a, sq, limit) - 1;; first -= 32) {
+      const int rt = first - lane;
+      const int units = rt >= 0 ? item_of<D>(a, sq, rt).units : 0;
+      int64_t upto = int64_t(units) * a.c.heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, off < upto);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          const int64_t rest = off - (upto - int64_t(units) * a.c.heads);
+          s_place = Place{s, rt, static_cast<int>(rest / units), static_cast<int>(rest % units)};
+        }
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, upto, 31);
+    }
   }
   if (warp == P::kSoft + P::kConv) {
     tc05::alloc(smem_u32(&s_tmem), 512);
@@ -196,6 +343,9 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
   __syncthreads();
   tc05::fence_after_sync();
   const uint32_t tmem = s_tmem;
+  Walk<D> w;
+  w.start(a, s_place, B - A);
+  const int d = a.c.d, chunks = d >> 4;
   // Warp-uniform: every lane has waited, or all give up.
   auto wait = [&](uint64_t* b, uint32_t parity, uint32_t flag) {
     const bool ok = *s_abort == 0 && mbar_wait_bounded(b, parity, wait_ns);
@@ -211,12 +361,19 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     // ------------------------------------------------------------ softmax
     more_registers<P::kSoftRegs>();
     const int mt = warp >> 2, r = 32 * (warp & 3) + lane, lr = 128 * mt + r;
-    const bool live = lr < rows;
-    const int row = row0 + lr, qi = row / a.group, hq = h * a.group + row - qi * a.group;
-    const int64_t grow = int64_t(sq.r0) + qi;
-    const int place = live ? past + qi : -1;
-    float fac;
-    {  // this thread's query, scaled by a power of two to below 2
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t t_o = tmem + lanes + P::kOCol + mt * D;
+    const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    bool ok = true;
+    int tick = 0;  // tiles of this CTA before
+    do {
+    if (w.empty()) continue;
+    const bool live = lr < w.it.rows;
+    const int row = w.it.row0 + lr, qi = row / a.group, hq = w.at.h * a.group + row - qi * a.group;
+    const int64_t grow = int64_t(w.sq.r0) + qi;
+    const int place = live ? w.it.past + qi : -1;
+    float fac = 0.f;
+    if (w.it.n > 0) {  // this thread's query, scaled by a power of two to below 2
       const uint4* qp = reinterpret_cast<const uint4*>(a.q + grow * a.q_stride + int64_t(hq) * d);
       constexpr int kAll = D / 8, kBatch = kAll < 16 ? kAll : 16;  // loads on their way at once
       uint4 u[kBatch];
@@ -257,23 +414,19 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.q_full);
     }
-    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t t_o = tmem + lanes + P::kOCol + mt * D;
-    const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     // of the 32 rows of this warp
-    const int w_lo = past + (row0 + 128 * mt + 32 * (warp & 3)) / a.group;
-    const int w_hi = past + min(row0 + 128 * mt + 32 * (warp & 3) + 31, all_rows - 1) / a.group;
+    const int first_row = w.it.row0 + 128 * mt + 32 * (warp & 3), all_rows = w.sq.n * a.group;
+    const int w_lo = w.it.past + first_row / a.group, w_hi = w.it.past + min(first_row + 31, all_rows - 1) / a.group;
+    const bool ragged = w.it.row0 + 128 * mt + 128 > all_rows || a.softcap > 0.f;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int slot = P::kMt == 2 ? mt : (i & 1);
-      if (!(ok = wait(&bar.s_full[slot], P::kMt == 2 ? (i & 1) : ((i >> 1) & 1), kErrWaitFull))) break;
+    for (int i = w.t0; i < w.t1; ++i, ++tick) {
+      const int slot = P::kMt == 2 ? mt : (tick & 1);
+      if (!(ok = wait(&bar.s_full[slot], P::kMt == 2 ? (tick & 1) : ((tick >> 1) & 1), kErrWaitFull))) break;
       tc05::fence_after_sync();
       const uint32_t t_s = tmem + lanes + slot * kT;
-      const TileScales& ts = s_scales[i % P::kSlots];
-      const int jt = j0 + i * kT;
-      const bool special =
-          a.softcap > 0.f || ts.dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window) || row0 + 128 * mt + 128 > all_rows;
+      const TileScales& ts = s_scales[tick % P::kSlots];
+      const int jt = w.it.j0 + i * kT;
+      const bool special = ragged || ts.dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
       // Scores of one 16-token group, capped and masked where needed; f: their factor.
       auto masked_scores = [&](float (&x)[16], int g, float& f) {
         const float4 sg = ts.group[g];
@@ -311,8 +464,8 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
         l *= k;
         m = x;
         vmax = ts.vmax;
-        if (i == 0) return true;
-        if (!wait(&bar.o_done[mt], (i - 1) & 1, kErrMma)) return false;
+        if (i == w.t0) return true;
+        if (!wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma)) return false;
         tc05::fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -337,18 +490,22 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       // tile is done over.
       uint32_t pk[kT / 2];
       float sum, big;
-      auto group = [&](auto score, float f, int g, float m0) {
+      // The special-function unit would take 2048 cycles of 256 rows' tile, as the products
+      // do; every fourth pair of exponentials goes to the multiply-add pipes instead.
+      auto group = [&](auto score, float f, int g, float m0, auto poly) {
         const float4 sg = ts.group[g];
         const uint64_t f2 = pair(f, f), c2 = pair(sg.y - m0, sg.y - m0);
         uint64_t s0 = 0, s1 = 0;
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const float2 x = unpair(fma2(score(e), f2, c2)), y = unpair(fma2(score(e + 2), f2, c2));
-          const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y), p2 = exp2_fast(y.x), p3 = exp2_fast(y.y);
-          s0 = add2(s0, pair(p0, p1));
-          s1 = add2(s1, pair(p2, p3));
-          pk[8 * g + e / 2] = f16x2(p0, p1);
-          pk[8 * g + e / 2 + 1] = f16x2(p2, p3);
+          const uint64_t x2 = fma2(score(e), f2, c2), y2 = fma2(score(e + 2), f2, c2);
+          const float2 x = unpair(x2), y = unpair(y2);
+          const float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          const float2 q = decltype(poly)::value && e % 8 == 4 ? exp2_poly(y2) : make_float2(exp2_fast(y.x), exp2_fast(y.y));
+          s0 = add2(s0, pair(p.x, p.y));
+          s1 = add2(s1, pair(q.x, q.y));
+          pk[8 * g + e / 2] = f16x2(p.x, p.y);
+          pk[8 * g + e / 2 + 1] = f16x2(q.x, q.y);
         }
         const float2 t = unpair(add2(s0, s1));
         big = fmaxf(big, t.x + t.y);
@@ -367,7 +524,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
               group([&](int e) { return pair(v[c & 1][16 * half + e], v[c & 1][16 * half + e + 1]); },
-                    fac * ts.group[2 * c + half].x, 2 * c + half, m0);
+                    fac * ts.group[2 * c + half].x, 2 * c + half, m0, std::true_type{});
           }
         } else {
 #pragma unroll
@@ -379,7 +536,7 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
             masked_scores(x, g, f);
-            group([&](int e) { return pair(x[e], x[e + 1]); }, f, g, m0);
+            group([&](int e) { return pair(x[e], x[e + 1]); }, f, g, m0, std::false_type{});  // masked: exactly 0
           }
         }
         if (!__any_sync(0xffffffffu, big > 32768.f)) break;
@@ -399,33 +556,54 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[slot]);
     }
-    // ---- outputs
-    if (ok && n > 0) ok = wait(&bar.o_done[mt], (n - 1) & 1, kErrMma);
-    if (ok) {
-      tc05::fence_after_sync();
-      const float inv = l > 0.f ? vmax * 0x1p-8f / l : (l == 0.f ? 0.f : l);
+    if (!ok) break;
+    // ---- outputs, or this piece's sums
+    const bool any = w.t0 < w.t1;
+    if (any && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
+    tc05::fence_after_sync();
+    const float unit = vmax * 0x1p-8f;
+    if (w.whole) {
+      const float inv = l > 0.f ? unit / l : (l == 0.f ? 0.f : l);
       uint16_t* op = a.out + grow * a.out_stride + int64_t(hq) * d;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32] = {};
-        if (n > 0) {
+        if (any) {
           tc05::ld_32x32b_x32(t_o + 32 * c, v);
           tc05::wait_ld();
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t w[4];
+          uint32_t x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
-            w[e] = *reinterpret_cast<const uint32_t*>(&b);
+            x[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          if (live && 2 * c + k / 2 < chunks) *reinterpret_cast<uint4*>(op + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (live && 2 * c + k / 2 < chunks) *reinterpret_cast<uint4*>(op + 32 * c + 8 * k) = make_uint4(x[0], x[1], x[2], x[3]);
         }
       }
       if (a.lse && live) a.lse[grow * (a.c.heads * a.group) + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      tc05::fence_before_sync();
+    } else {
+      float* part = scr.joined + int64_t(2 * cta + (w.t0 > 0 ? 0 : 1)) * scr.slot_floats;
+      if (live) *reinterpret_cast<float2*>(part + scr.rows * d + 2 * lr) = make_float2(m, l);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tc05::ld_32x32b_x32(t_o + 32 * c, v);
+        tc05::wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (live && 2 * c + k / 4 < chunks)
+            *reinterpret_cast<float4*>(part + int64_t(lr) * d + 32 * c + 4 * k) =
+                make_float4(__uint_as_float(v[4 * k]) * unit, __uint_as_float(v[4 * k + 1]) * unit, __uint_as_float(v[4 * k + 2]) * unit,
+                            __uint_as_float(v[4 * k + 3]) * unit);
+      }
+      if (w.t0 == 0 && tid == 0)  // the item goes on in the next CTAs
+        scr.open[cta] = Open{w.sq.r0, w.it.row0, w.at.h, w.it.rows, cut.part(B - 1 + (w.it.n - w.t1)) - cta + 1};
     }
+    tc05::fence_before_sync();
+    } while (w.next(a, limit));
   } else if (warp < P::kSoft + P::kConv) {
     // ------------------------------------------------------------ bytes to fp16
     fewer_registers<P::kConvRegs>();
@@ -440,29 +618,32 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     const int page = a.c.page, log2p = a.c.page_log2;
     // lane g < kGroups: the page of group g of a tile
     auto page_of = [&](int i) {
-      const int j = j0 + i * kT + 16 * lane;
-      return lane < P::kGroups && j < j1 && j + 16 > lo ? a.b.pages[int64_t(s) * a.b.max_pages + (j >> log2p)] : -1;
+      const int j = w.it.j0 + i * kT + 16 * lane;
+      return lane < P::kGroups && j < w.it.j1 && j + 16 > w.it.lo ? a.b.pages[int64_t(w.at.s) * a.b.max_pages + (j >> log2p)] : -1;
     };
     // checked where it is used, so that the load runs ahead
     auto checked = [&](int pid, int i) {
-      const int j = j0 + i * kT + 16 * lane;
+      const int j = w.it.j0 + i * kT + 16 * lane;
       if (pid >= 0 && pid < a.c.n_pages) return pid;
-      if (lane < P::kGroups && j < j1 && j + 16 > lo) atomicOr(a.err, kErrBounds);
+      if (lane < P::kGroups && j < w.it.j1 && j + 16 > w.it.lo) atomicOr(a.err, kErrBounds);
       return -1;
     };
     uint4 xk[kIt], xv[kIt];
     float2 sc = make_float2(0.f, 0.f);  // lane's group: K, V scale
+    const uint32_t mine = tk * d + 16 * c;
     auto fetch = [&](int i, int pid) {
-      const int64_t tl = int64_t(pid) * a.c.heads + h;
+      // where this lane's group starts in the cache (-1: nowhere)
+      const int64_t tl = int64_t(pid) * a.c.heads + w.at.h;
+      const int64_t group = pid < 0 ? -1 : (tl * page + ((w.it.j0 + i * kT + 16 * lane) & (page - 1))) * d;
       sc = make_float2(0.f, 0.f);
       if (pid >= 0) sc = make_float2(__ldg(a.c.k_scale + tl), __ldg(a.c.v_scale + tl));
 #pragma unroll
       for (int k = 0; k < kIt; ++k) {
-        const int tok = cw * kTokens + k * kAt + tk, j = j0 + i * kT + tok;
-        const int p = __shfl_sync(0xffffffffu, pid, (cw * kTokens + k * kAt) >> 4);
+        const int first = cw * kTokens + k * kAt;  // token of the tile
+        const int64_t at = __shfl_sync(0xffffffffu, group, first >> 4);
         xk[k] = xv[k] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        if (p >= 0 && c < chunks) {
-          const int64_t off = ((int64_t(p) * a.c.heads + h) * page + (j & (page - 1))) * d + 16 * c;
+        if (at >= 0 && c < chunks) {
+          const int64_t off = at + ((first & 15) * d + mine);
           xk[k] = *reinterpret_cast<const uint4*>(a.c.k + off);
           xv[k] = *reinterpret_cast<const uint4*>(a.c.v + off);
         }
@@ -481,14 +662,18 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       fence_async_smem();
       __syncwarp();
     };
+    int tick = 0;
+    bool ok = true;
+    do {
+    if (w.empty() || w.it.n == 0) continue;
     float vmax = kTinyScale;
-    int pid = n > 0 ? checked(page_of(0), 0) : -1;
-    if (n > 0) fetch(0, pid);
-    int next = n > 1 ? page_of(1) : -1;
-    for (int i = 0; i < n; ++i) {
-      const int b = i & 1;
-      const uint32_t parity = ((i >> 1) & 1) ^ 1;
-      if (i >= 2 && !wait(&bar.k_empty[b], parity, kErrWaitEmpty)) break;
+    int pid = checked(page_of(w.t0), w.t0);
+    fetch(w.t0, pid);
+    int next = w.t0 + 1 < w.t1 ? page_of(w.t0 + 1) : -1;
+    for (int i = w.t0; i < w.t1; ++i, ++tick) {
+      const int b = tick & 1;
+      const uint32_t parity = ((tick >> 1) & 1) ^ 1;
+      if (tick >= 2 && !(ok = wait(&bar.k_empty[b], parity, kErrWaitEmpty))) break;
       if (cw == 0) {  // the tile's scales
         float top = lane < P::kGroups ? sc.y : 0.f;
 #pragma unroll
@@ -498,10 +683,10 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
           vmax = __int_as_float(min(e, 254) << 23);
         }
         const float lg = log2f(fmaxf(sc.y / vmax, 0x1p-60f)) + kPLog2;
-        TileScales& ts = s_scales[i % P::kSlots];
-        const int j = j0 + i * kT + 16 * lane;
+        TileScales& ts = s_scales[tick % P::kSlots];
+        const int j = w.it.j0 + i * kT + 16 * lane;
         if (lane < P::kGroups) ts.group[lane] = make_float4(sc.x, lg, exp2f(-lg), pid >= 0 ? 1.f : 0.f);
-        const bool dead = __any_sync(0xffffffffu, lane < P::kGroups && j < j1 && pid < 0);
+        const bool dead = __any_sync(0xffffffffu, lane < P::kGroups && j < w.it.j1 && pid < 0);
         if (lane == 0) {
           ts.vmax = vmax;
           ts.dead = dead;
@@ -509,21 +694,22 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
       }
       spread(sk_base + b * P::kKvBytes, xk);
       if (lane == 0) mbar_arrive(&bar.k_full[b]);
-      if (i >= 2 && !wait(&bar.v_empty[b], parity, kErrWaitEmpty)) break;
+      if (tick >= 2 && !(ok = wait(&bar.v_empty[b], parity, kErrWaitEmpty))) break;
       spread(sv_base + b * P::kKvBytes, xv);
       if (lane == 0) mbar_arrive(&bar.v_full[b]);
-      if (i + 1 < n) {
+      if (i + 1 < w.t1) {
         pid = checked(next, i + 1);
         fetch(i + 1, pid);
-        if (i + 2 < n) next = page_of(i + 2);
+        if (i + 2 < w.t1) next = page_of(i + 2);
       }
     }
+    } while (ok && w.next(a, limit));
   } else {
     // ------------------------------------------------------------ products
     fewer_registers<P::kMmaRegs>();
     // The whole warp walks the loop, so that descriptors stay in uniform registers
     // (a lone thread's moves to them cost more than the products); one lane issues.
-    if (warp == P::kSoft + P::kConv && n > 0) {
+    if (warp == P::kSoft + P::kConv) {
     const bool leader = elect_one();
     auto wait1 = [&](uint64_t* b, uint32_t parity) { return wait(b, parity, kErrMma); };
     auto commit = [&](uint64_t* b) {
@@ -533,8 +719,8 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
     // One thread issues every product: their descriptors are sums of a base and constants (16-byte units).
     const uint64_t desc_q = tc05::desc_kmajor_sw128(sq_base), desc_k = tc05::desc_kmajor_sw128(sk_base);
     const uint64_t desc_v = tc05::desc_mnmajor_sw128(sv_base, P::kBlocks > 1 ? P::kKvBlock : 1024);
-    auto scores = [&](int mt, int slot, int i) {  // S = Q K^T of tile i
-      const uint64_t q = desc_q + mt * (P::kBlocks * P::kQBlock >> 4), k0 = desc_k + (i & 1) * (P::kKvBytes >> 4);
+    auto scores = [&](int mt, int slot, int tick) {  // S = Q K^T
+      const uint64_t q = desc_q + mt * (P::kBlocks * P::kQBlock >> 4), k0 = desc_k + (tick & 1) * (P::kKvBytes >> 4);
       const uint32_t to = tmem + slot * kT;
       if (leader) {
 #pragma unroll
@@ -544,61 +730,65 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
         tc05::commit(smem_u32(&bar.s_full[slot]));
       }
     };
-    auto outputs = [&](int mt, int slot, int i) {  // O += P V of tile i
-      const uint64_t v0 = desc_v + (i & 1) * (P::kKvBytes >> 4);
+    auto outputs = [&](int mt, int slot, int tick, bool first) {  // O += P V
+      const uint64_t v0 = desc_v + (tick & 1) * (P::kKvBytes >> 4);
       const uint32_t to = tmem + P::kOCol + mt * D, p = tmem + slot * kT;
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < kT / 16; ++k) tc05::mma_ts(to, p + 8 * k, v0 + (k * 2048 >> 4), id_o, i > 0 || k > 0);
+        for (int k = 0; k < kT / 16; ++k) tc05::mma_ts(to, p + 8 * k, v0 + (k * 2048 >> 4), id_o, !first || k > 0);
         tc05::commit(smem_u32(&bar.o_done[mt]));
       }
     };
-    auto full = [&](uint64_t (&b)[2], int i) {
-      if (!wait1(&b[i & 1], (i >> 1) & 1)) return false;
+    auto full = [&](uint64_t (&b)[2], int tick) {
+      if (!wait1(&b[tick & 1], (tick >> 1) & 1)) return false;
       tc05::fence_after_sync();
       return true;
     };
-    bool ok = wait1(&bar.q_full, 0);
-    if constexpr (P::kMt == 2) {
-      ok = ok && full(bar.k_full, 0);
-      if (ok) {
-        scores(0, 0, 0);
-        scores(1, 1, 0);
-        commit(&bar.k_empty[0]);
-      }
-      for (int i = 0; ok && i < n; ++i) {
+    bool ok = true;
+    int tick = 0, pieces = 0;
+    do {
+      if (w.empty() || w.it.n == 0) continue;  // nothing, or rows that see no token
+      if (!(ok = wait1(&bar.q_full, pieces++ & 1))) break;
+      const int n = w.t1 - w.t0;
+      if constexpr (P::kMt == 2) {
+        if (!(ok = full(bar.k_full, tick))) break;
+        scores(0, 0, tick);
+        scores(1, 1, tick);
+        commit(&bar.k_empty[tick & 1]);
+        for (int i = 0; ok && i < n; ++i, ++tick) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          if (mt == 0 && !(ok = full(bar.v_full, i))) break;
-          if (!(ok = wait1(&bar.p_full[mt], i & 1))) break;
+          for (int mt = 0; mt < 2; ++mt) {
+            if (mt == 0 && !(ok = full(bar.v_full, tick))) break;
+            if (!(ok = wait1(&bar.p_full[mt], tick & 1))) break;
+            tc05::fence_after_sync();
+            outputs(mt, mt, tick, i == 0);
+            if (mt == 1) commit(&bar.v_empty[tick & 1]);
+            if (i + 1 < n) {
+              if (mt == 0 && !(ok = full(bar.k_full, tick + 1))) break;
+              scores(mt, mt, tick + 1);
+              if (mt == 1) commit(&bar.k_empty[(tick + 1) & 1]);
+            }
+          }
+        }
+      } else {
+        for (int i = 0; i < 2 && i < n; ++i) {
+          if (!(ok = full(bar.k_full, tick + i))) break;
+          scores(0, (tick + i) & 1, tick + i);
+          commit(&bar.k_empty[(tick + i) & 1]);
+        }
+        for (int i = 0; ok && i < n; ++i, ++tick) {
+          if (!(ok = full(bar.v_full, tick) && wait1(&bar.p_full[tick & 1], (tick >> 1) & 1))) break;
           tc05::fence_after_sync();
-          outputs(mt, mt, i);
-          if (mt == 1) commit(&bar.v_empty[i & 1]);
-          if (i + 1 < n) {
-            if (mt == 0 && !(ok = full(bar.k_full, i + 1))) break;
-            scores(mt, mt, i + 1);
-            if (mt == 1) commit(&bar.k_empty[(i + 1) & 1]);
+          outputs(0, tick & 1, tick, i == 0);
+          commit(&bar.v_empty[tick & 1]);
+          if (i + 2 < n) {
+            if (!(ok = full(bar.k_full, tick + 2))) break;
+            scores(0, tick & 1, tick + 2);
+            commit(&bar.k_empty[tick & 1]);
           }
         }
       }
-    } else {
-      for (int i = 0; ok && i < 2 && i < n; ++i) {
-        if (!(ok = full(bar.k_full, i))) break;
-        scores(0, i, i);
-        commit(&bar.k_empty[i]);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        if (!(ok = full(bar.v_full, i) && wait1(&bar.p_full[i & 1], (i >> 1) & 1))) break;
-        tc05::fence_after_sync();
-        outputs(0, i & 1, i);
-        commit(&bar.v_empty[i & 1]);
-        if (i + 2 < n) {
-          if (!(ok = full(bar.k_full, i + 2))) break;
-          scores(0, i & 1, i + 2);
-          commit(&bar.k_empty[i & 1]);
-        }
-      }
-    }
+    } while (ok && w.next(a, limit));
     // all products that this thread issued have finished before the CTA moves on
     commit(&bar.drain);
     if (!mbar_wait_bounded(&bar.drain, 0, 1000000000ull) && leader) atomicOr(a.err, kErrDrain);
@@ -611,24 +801,52 @@ kv_prompt_kernel(const AttendArgs a, int limit, int tiles_max, uint64_t wait_ns)
   }
 }
 
+// Joins the items that several CTAs shared, a warp a row.
+constexpr int kJoinWarps = 4;
 template <int D>
-cudaError_t launch(const AttendArgs& a, int limit, cudaStream_t stream) {
+__global__ void __launch_bounds__(kJoinWarps * 32)
+kv_prompt_join_kernel(const AttendArgs a, const Scratch sc) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int c = blockIdx.x;
+  const Open p = sc.open[c];
+  for (int lr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); lr < p.rows; lr += gridDim.y * kJoinWarps) {
+    Joined<D> r;
+    join_row<D>(sc.rows, a.c.d, lr, p.n, [&](int k) { return sc.joined + int64_t(2 * (c + k) + (k == 0 ? 1 : 0)) * sc.slot_floats; }, r);
+    write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
+  }
+}
+
+template <int D>
+size_t layout(const KvCache& c, const KvBatch& b, int group, int sms, Scratch* sc = nullptr, uint8_t* base = nullptr) {
+  const int rows = part_rows(b.max_new, group, Plan<D>::kRows), floats = part_floats(rows, c.d);
+  const size_t open = align256(size_t(sms) * sizeof(Open));
+  if (sc) *sc = Scratch{nullptr, reinterpret_cast<float*>(base + open), reinterpret_cast<Open*>(base), rows, floats};
+  return open + align256(size_t(2) * sms * floats * 4);
+}
+
+template <int D>
+cudaError_t launch(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms) {
   using P = Plan<D>;
   cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t rows = int64_t(a.b.max_new) * a.group, tiles = (rows + P::kRows - 1) / P::kRows;
-  const int64_t grid = tiles * a.c.heads * a.b.n_seqs;
-  if (grid > 0x7fffffff) return cudaErrorNotSupported;
-  return launch_pdl(kv_prompt_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(P::kThreads), P::kSmem, stream, a, limit,
-                    static_cast<int>(tiles), wait_limit_ns());
+  Scratch sc;
+  layout<D>(a.c, a.b, a.group, sms, &sc, scratch);
+  e = launch_pdl(kv_prompt_kernel<D>, dim3(sms), dim3(P::kThreads), P::kSmem, stream, a, sc, limit, wait_limit_ns());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_prompt_join_kernel<D>, dim3(sms, 16), dim3(kJoinWarps * 32), 0, stream, a, sc);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, cudaStream_t stream) {
-  if (a.c.d <= 64) return launch<64>(a, limit, stream);
-  if (a.c.d <= 128) return launch<128>(a, limit, stream);
-  return launch<256>(a, limit, stream);
+size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms) {
+  return c.d <= 64 ? layout<64>(c, b, group, sms) : c.d <= 128 ? layout<128>(c, b, group, sms) : layout<256>(c, b, group, sms);
+}
+
+cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms) {
+  if (a.c.d <= 64) return launch<64>(a, limit, scratch, stream, sms);
+  if (a.c.d <= 128) return launch<128>(a, limit, scratch, stream, sms);
+  return launch<256>(a, limit, scratch, stream, sms);
 }
 
 }  // namespace mq
