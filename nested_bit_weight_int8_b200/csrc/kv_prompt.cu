@@ -136,15 +136,16 @@ struct Plan {
 };
 
 struct TileScales {
-  float4 group[8];  // K scale, log2 of V's factor, 1 / that factor, 1 where the page may be read
+  float4 group[4];  // of two groups each: K scale, log2 of V's factor
   float vmax;
-  int dead;         // some group may not be read
+  int dead;         // a bit for each group that may not be read
 };
 
 struct Bars {
   uint64_t q_full;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t sc_full[4];
   uint64_t drain;
 };
 
@@ -253,6 +254,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_done[i], 1);
     }
+    for (int i = 0; i < P::kSlots; ++i) mbar_init(&bar.sc_full[i], 1);
     mbar_init(&bar.drain, 1);
     s_abort_word = 0;
     s_pre[0] = 0;
@@ -419,36 +421,51 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const int w_lo = w.it.past + first_row / a.group, w_hi = w.it.past + min(first_row + 31, all_rows - 1) / a.group;
     const bool ragged = w.it.row0 + 128 * mt + 128 > all_rows || a.softcap > 0.f;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
+    // a tile's scales, taken while its scores are still being made: the products keep
+    // shared memory busy, and a load waits for hundreds of cycles
+    float fs[P::kGroups], lg[P::kGroups], tile_vmax;
+    int dead;
+    auto take = [&](int tick) {
+      const int slot = tick % P::kSlots;
+      if (!wait(&bar.sc_full[slot], (tick / P::kSlots) & 1, kErrWaitFull)) return false;
+      const TileScales& ts = s_scales[slot];
+#pragma unroll
+      for (int g = 0; g < P::kGroups; g += 2) {
+        const float4 x = ts.group[g / 2];
+        fs[g] = fac * x.x, lg[g] = x.y, fs[g + 1] = fac * x.z, lg[g + 1] = x.w;
+      }
+      tile_vmax = ts.vmax;
+      dead = ts.dead;
+      return true;
+    };
+    if (w.t0 < w.t1 && !(ok = take(tick))) break;
     for (int i = w.t0; i < w.t1; ++i, ++tick) {
       const int slot = P::kMt == 2 ? mt : (tick & 1);
       if (!(ok = wait(&bar.s_full[slot], P::kMt == 2 ? (tick & 1) : ((tick >> 1) & 1), kErrWaitFull))) break;
       tc05::fence_after_sync();
       const uint32_t t_s = tmem + lanes + slot * kT;
-      const TileScales& ts = s_scales[tick % P::kSlots];
       const int jt = w.it.j0 + i * kT;
-      const bool special = ragged || ts.dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
+      const bool special = ragged || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
       // Scores of one 16-token group, capped and masked where needed; f: their factor.
       auto masked_scores = [&](float (&x)[16], int g, float& f) {
-        const float4 sg = ts.group[g];
-        f = fac * sg.x;
         if (!special) return;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float y = x[e] * f;
           if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
           const int j = jt + 16 * g + e;
-          x[e] = j > place || (a.window > 0 && j <= place - a.window) || sg.w == 0.f ? -INFINITY : y;
+          x[e] = j > place || (a.window > 0 && j <= place - a.window) || ((dead >> g) & 1) ? -INFINITY : y;
         }
         f = 1.f;
       };
       auto largest = [&]() {  // score of the tile
         float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll
         for (int g = 0; g < P::kGroups; ++g) {
           uint32_t v[16];
           tc05::ld_32x32b_x16(t_s + 16 * g, v);
           tc05::wait_ld();
-          float x[16], f;
+          float x[16], f = fs[g];
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
           masked_scores(x, g, f);
@@ -460,10 +477,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // Raises the maximum (an integer, so that the factors are powers of two) to
       // `top` and the V scale to the tile's; O follows.
       auto raise = [&](float top) -> bool {
-        const float x = fmaxf(ceilf(top), m), k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / ts.vmax);
+        const float x = fmaxf(ceilf(top), m), k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / tile_vmax);
         l *= k;
         m = x;
-        vmax = ts.vmax;
+        vmax = tile_vmax;
         if (i == w.t0) return true;
         if (!wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma)) return false;
         tc05::fence_after_sync();
@@ -481,7 +498,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       };
       // rows that have seen nothing yet take this tile's maximum first
       const bool fresh = __any_sync(0xffffffffu, live && m == -INFINITY);
-      if (fresh || ts.vmax != vmax) {
+      if (fresh || tile_vmax != vmax) {
         if (!(ok = raise(fresh ? largest() : -INFINITY))) break;
       }
       // p' of the whole tile, in registers: no branch between its scores, so that their
@@ -493,8 +510,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // The special-function unit would take 2048 cycles of 256 rows' tile, as the products
       // do; every fourth pair of exponentials goes to the multiply-add pipes instead.
       auto group = [&](auto score, float f, int g, float m0, auto poly) {
-        const float4 sg = ts.group[g];
-        const uint64_t f2 = pair(f, f), c2 = pair(sg.y - m0, sg.y - m0);
+        const uint64_t f2 = pair(f, f), c2 = pair(lg[g] - m0, lg[g] - m0);
         uint64_t s0 = 0, s1 = 0;
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
@@ -509,7 +525,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         }
         const float2 t = unpair(add2(s0, s1));
         big = fmaxf(big, t.x + t.y);
-        sum = fmaf(t.x + t.y, sg.z, sum);
+        sum = fmaf(t.x + t.y, exp2_fast(-lg[g]), sum);
       };
       while (true) {
         const float m0 = m == -INFINITY ? 0.f : m;
@@ -524,7 +540,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
 #pragma unroll
             for (int half = 0; half < 2; ++half)
               group([&](int e) { return pair(v[c & 1][16 * half + e], v[c & 1][16 * half + e + 1]); },
-                    fac * ts.group[2 * c + half].x, 2 * c + half, m0, std::true_type{});
+                    fs[2 * c + half], 2 * c + half, m0, std::true_type{});
           }
         } else {
 #pragma unroll
@@ -532,7 +548,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
             uint32_t v[16];
             tc05::ld_32x32b_x16(t_s + 16 * g, v);
             tc05::wait_ld();
-            float x[16], f;
+            float x[16], f = fs[g];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
             masked_scores(x, g, f);
@@ -555,10 +571,14 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       tc05::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+      if (i + 1 < w.t1 && !(ok = take(tick + 1))) break;
     }
     if (!ok) break;
     // ---- outputs, or this piece's sums
     const bool any = w.t0 < w.t1;
+    // A warp may be done with a piece's last tile while the products of the one before
+    // still run (S twice in turn): that phase first, a barrier's wait tells only two apart.
+    if (P::kMt == 1 && w.t1 - w.t0 > 1 && !(ok = wait(&bar.o_done[mt], tick & 1, kErrMma))) break;
     if (any && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
     tc05::fence_after_sync();
     const float unit = vmax * 0x1p-8f;
@@ -685,12 +705,14 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         const float lg = log2f(fmaxf(sc.y / vmax, 0x1p-60f)) + kPLog2;
         TileScales& ts = s_scales[tick % P::kSlots];
         const int j = w.it.j0 + i * kT + 16 * lane;
-        if (lane < P::kGroups) ts.group[lane] = make_float4(sc.x, lg, exp2f(-lg), pid >= 0 ? 1.f : 0.f);
-        const bool dead = __any_sync(0xffffffffu, lane < P::kGroups && j < w.it.j1 && pid < 0);
+        if (lane < P::kGroups) reinterpret_cast<float2*>(ts.group)[lane] = make_float2(sc.x, lg);
+        const unsigned dead = __ballot_sync(0xffffffffu, lane < P::kGroups && j < w.it.j1 && pid < 0);
         if (lane == 0) {
           ts.vmax = vmax;
-          ts.dead = dead;
+          ts.dead = static_cast<int>(dead);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.sc_full[tick % P::kSlots]);
       }
       spread(sk_base + b * P::kKvBytes, xk);
       if (lane == 0) mbar_arrive(&bar.k_full[b]);

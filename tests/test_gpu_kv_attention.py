@@ -183,6 +183,19 @@ def test_the_same_call_gives_the_same_bits_and_strides_do_not_matter():
         assert torch.equal(o, outs[0][0]) and (l is None or torch.equal(l, outs[0][1]))
 
 
+@pytest.mark.parametrize("heads,group,dim,page", [(1, 1, 64, 16), (2, 4, 128, 64), (1, 1, 192, 64), (1, 2, 256, 32)])
+def test_prompts_give_the_same_bits_every_time(heads, group, dim, page):
+    seqs = [(300, 300), (1, 500), (129, 700), (65, 65), (257, 900)]
+    b = Batch(seqs, heads, dim, page, seed=11, fill="all")
+    q = queries(b, heads * group)
+    out, log = attend(b, heads * group, q)
+    check(b, heads * group, q, out, log)
+    for _ in range(60):
+        again, log2 = attend(b, heads * group, q)
+        assert torch.equal(out, again) and torch.equal(log, log2)
+    mq.device_status()
+
+
 def test_two_streams_and_a_graph_that_sees_new_lengths():
     b = Batch([(1, 700), (1, 90)], 2, 128, 64, seed=10, fill="all")
     q = queries(b, 8)
