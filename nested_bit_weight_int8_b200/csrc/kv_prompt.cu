@@ -136,7 +136,7 @@ struct Plan {
 };
 
 struct TileScales {
-  float4 group[4];  // of two groups each: K scale, log2 of V's factor
+  float2 group[8];  // K scale, log2 of V's factor
   float vmax;
   int dead;         // a bit for each group that may not be read
 };
@@ -146,6 +146,7 @@ struct Bars {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t sc_full[4];
+  uint64_t plan_full[2], plan_empty[2];
   uint64_t drain;
 };
 
@@ -180,6 +181,16 @@ __device__ __forceinline__ int item_rows(const AttendArgs& a, const Seq& sq, int
   return all <= limit ? 0 : (all + Plan<D>::kRows - 1) / Plan<D>::kRows;
 }
 
+// A piece of an item, as the CTA's warps take it from shared memory.
+struct Piece {
+  int s, h, r0;           // sequence, head, the sequence's first row
+  int row0, rows, all;    // of the sequence: the item's rows, all rows
+  int past;               // place of the sequence's first row
+  int lo, j0, j1;         // the item's tokens
+  int n, t0, t1;          // its tiles, and the piece's; n < 0: the range is done
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
+};
+
 // A CTA's way through its range: sequences, their row tiles from the last, heads.
 struct Place {
   int s, rt, h, u0;
@@ -191,13 +202,11 @@ struct Walk {
   Item it;
   int64_t left;  // units of the range
   int t0, t1;    // tiles of the piece
-  bool whole;
   __device__ __forceinline__ void piece() {
     const int u1 = static_cast<int>(min(int64_t(it.units), at.u0 + left));
     t0 = max(at.u0 - it.start, 0);
     t1 = max(u1 - it.start, 0);
     if (it.n == 0) t0 = t1 = 0;
-    whole = t0 == 0 && t1 == it.n;
   }
   __device__ __forceinline__ bool empty() const { return it.n > 0 && t0 >= t1; }
   __device__ __forceinline__ void start(const AttendArgs& a, const Place& p, int64_t units) {
@@ -235,7 +244,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   __shared__ Bars bar;
   __shared__ TileScales s_scales[P::kSlots];
   __shared__ int64_t s_pre[kThreads + 1], s_warp[kWarps];
-  __shared__ Place s_place;
+  __shared__ Piece s_piece[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort_word;
   volatile int* s_abort = &s_abort_word;
@@ -255,6 +264,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < P::kSlots; ++i) mbar_init(&bar.sc_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.plan_full[i], 1);
+      mbar_init(&bar.plan_empty[i], P::kSoft + P::kConv + 1);
+    }
     mbar_init(&bar.drain, 1);
     s_abort_word = 0;
     s_pre[0] = 0;
@@ -305,38 +318,6 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   if (cta >= ctas || total == 0) return;
   const Cut cut(total, ctas);
   const int64_t A = cut.first(cta), B = cut.first(cta + 1);
-  if (warp == 0) {
-    int run = (__popc(__ballot_sync(0xffffffffu, s_pre[lane * kWarps] <= A)) - 1) * kWarps;
-    run += __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_pre[run + lane] <= A)) - 1;
-    int s = run * per;
-    int64_t off = A - s_pre[run];
-    while (true) {
-      const int64_t u = seq_units(s);
-      if (off < u) break;
-      off -= u;
-      ++s;
-    }
-    const Seq sq = load_seq(a.b, s, nullptr);
-    for (int first = item_rows<D>(a, sq, limit) - 1;; first -= 32) {
-      const int rt = first - lane;
-      const int units = rt >= 0 ? item_of<D>(a, sq, rt).units : 0;
-      int64_t upto = int64_t(units) * a.c.heads;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += up;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, off < upto);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          const int64_t rest = off - (upto - int64_t(units) * a.c.heads);
-          s_place = Place{s, rt, static_cast<int>(rest / units), static_cast<int>(rest % units)};
-        }
-        break;
-      }
-      off -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-  }
   if (warp == P::kSoft + P::kConv) {
     tc05::alloc(smem_u32(&s_tmem), 512);
     tc05::relinquish();
@@ -345,8 +326,6 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   __syncthreads();
   tc05::fence_after_sync();
   const uint32_t tmem = s_tmem;
-  Walk<D> w;
-  w.start(a, s_place, B - A);
   const int d = a.c.d, chunks = d >> 4;
   // Warp-uniform: every lane has waited, or all give up.
   auto wait = [&](uint64_t* b, uint32_t parity, uint32_t flag) {
@@ -359,6 +338,15 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     return false;
   };
 
+  // The CTA's k-th piece, or false at the end.
+  auto piece_of = [&](int k, Piece& p) {
+    if (!wait(&bar.plan_full[k & 1], (k >> 1) & 1, kErrWaitFull)) return false;
+    p = s_piece[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.plan_empty[k & 1]);
+    return p.n >= 0;
+  };
+
   if (warp < P::kSoft) {
     // ------------------------------------------------------------ softmax
     more_registers<P::kSoftRegs>();
@@ -368,14 +356,14 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     bool ok = true;
     int tick = 0;  // tiles of this CTA before
-    do {
-    if (w.empty()) continue;
-    const bool live = lr < w.it.rows;
-    const int row = w.it.row0 + lr, qi = row / a.group, hq = w.at.h * a.group + row - qi * a.group;
-    const int64_t grow = int64_t(w.sq.r0) + qi;
-    const int place = live ? w.it.past + qi : -1;
+    Piece w;
+    for (int k = 0; piece_of(k, w); ++k) {
+    const bool live = lr < w.rows;
+    const int row = w.row0 + lr, qi = row / a.group, hq = w.h * a.group + row - qi * a.group;
+    const int64_t grow = int64_t(w.r0) + qi;
+    const int place = live ? w.past + qi : -1;
     float fac = 0.f;
-    if (w.it.n > 0) {  // this thread's query, scaled by a power of two to below 2
+    if (w.n > 0) {  // this thread's query, scaled by a power of two to below 2
       const uint4* qp = reinterpret_cast<const uint4*>(a.q + grow * a.q_stride + int64_t(hq) * d);
       constexpr int kAll = D / 8, kBatch = kAll < 16 ? kAll : 16;  // loads on their way at once
       uint4 u[kBatch];
@@ -417,23 +405,20 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       if (lane == 0) mbar_arrive(&bar.q_full);
     }
     // of the 32 rows of this warp
-    const int first_row = w.it.row0 + 128 * mt + 32 * (warp & 3), all_rows = w.sq.n * a.group;
-    const int w_lo = w.it.past + first_row / a.group, w_hi = w.it.past + min(first_row + 31, all_rows - 1) / a.group;
-    const bool ragged = w.it.row0 + 128 * mt + 128 > all_rows || a.softcap > 0.f;
+    const int first_row = w.row0 + 128 * mt + 32 * (warp & 3);
+    const int w_lo = w.past + first_row / a.group, w_hi = w.past + min(first_row + 31, w.all - 1) / a.group;
+    const bool ragged = w.row0 + 128 * mt + 128 > w.all || a.softcap > 0.f;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
-    // a tile's scales, taken while its scores are still being made: the products keep
-    // shared memory busy, and a load waits for hundreds of cycles
-    float fs[P::kGroups], lg[P::kGroups], tile_vmax;
-    int dead;
+    // A tile's scales, lane g group g's, taken while its scores are still being made: the
+    // products keep shared memory busy, and a load waits for hundreds of cycles.
+    float2 scale = make_float2(0.f, 0.f);
+    float tile_vmax = 0.f;
+    int dead = 0;
     auto take = [&](int tick) {
       const int slot = tick % P::kSlots;
       if (!wait(&bar.sc_full[slot], (tick / P::kSlots) & 1, kErrWaitFull)) return false;
       const TileScales& ts = s_scales[slot];
-#pragma unroll
-      for (int g = 0; g < P::kGroups; g += 2) {
-        const float4 x = ts.group[g / 2];
-        fs[g] = fac * x.x, lg[g] = x.y, fs[g + 1] = fac * x.z, lg[g + 1] = x.w;
-      }
+      if (lane < P::kGroups) scale = ts.group[lane];
       tile_vmax = ts.vmax;
       dead = ts.dead;
       return true;
@@ -444,129 +429,139 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       if (!(ok = wait(&bar.s_full[slot], P::kMt == 2 ? (tick & 1) : ((tick >> 1) & 1), kErrWaitFull))) break;
       tc05::fence_after_sync();
       const uint32_t t_s = tmem + lanes + slot * kT;
-      const int jt = w.it.j0 + i * kT;
+      const int jt = w.j0 + i * kT;
       const bool special = ragged || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
-      // Scores of one 16-token group, capped and masked where needed; f: their factor.
-      auto masked_scores = [&](float (&x)[16], int g, float& f) {
-        if (!special) return;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float y = x[e] * f;
-          if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
-          const int j = jt + 16 * g + e;
-          x[e] = j > place || (a.window > 0 && j <= place - a.window) || ((dead >> g) & 1) ? -INFINITY : y;
-        }
-        f = 1.f;
+      auto factor = [&](int g) { return fac * __shfl_sync(0xffffffffu, scale.x, g); };
+      // A score of group g, scaled, capped and masked (where some row of the warp needs it).
+      auto masked = [&](uint32_t v, float f, int g, int e) {
+        float y = __uint_as_float(v) * f;
+        if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
+        const int j = jt + 16 * g + e;
+        return j > place || (a.window > 0 && j <= place - a.window) || ((dead >> g) & 1) ? -INFINITY : y;
       };
-      auto largest = [&]() {  // score of the tile
+      auto largest = [&](int g0, int g1) {  // score of groups g0 .. g1 - 1
         float top = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < P::kGroups; ++g) {
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
           uint32_t v[16];
           tc05::ld_32x32b_x16(t_s + 16 * g, v);
           tc05::wait_ld();
-          float x[16], f = fs[g];
+          const float f = factor(g);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
-          masked_scores(x, g, f);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e] * f);
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, special ? masked(v[e], f, g, e) : __uint_as_float(v[e]) * f);
         }
         return top;
       };
-      // Raises the maximum (an integer, so that the factors are powers of two) to
-      // `top` and the V scale to the tile's; O follows.
-      auto raise = [&](float top) -> bool {
+      // Raises the maximum (an integer, so that the factors are powers of two) to `top` and
+      // the V scale to the tile's; O, and the columns of P that are written, follow.
+      float sum = 0.f;
+      auto raise = [&](float top, int done) -> bool {
         const float x = fmaxf(ceilf(top), m), k = x == -INFINITY ? 1.f : exp2_fast(m - x), kv = k * (vmax / tile_vmax);
         l *= k;
+        sum *= k;
         m = x;
         vmax = tile_vmax;
-        if (i == w.t0) return true;
-        if (!wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma)) return false;
-        tc05::fence_after_sync();
+        const __half2 k2 = __float2half2_rn(k);
+        tc05::wait_st();  // P so far
 #pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t v[16];
-          tc05::ld_32x32b_x16(t_o + 16 * c, v);
+        for (int c = 0; c < done; c += 8) {
+          uint32_t v[8];
+          tc05::ld_32x32b_x8(t_s + c, v);
           tc05::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
-          tc05::st_32x32b_x16(t_o + 16 * c, v);
+          for (int e = 0; e < 8; ++e) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), k2);
+            v[e] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          tc05::st_32x32b_x8(t_s + c, v);
+        }
+        if (i > w.t0) {
+          if (!wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma)) return false;
+          tc05::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t v[16];
+            tc05::ld_32x32b_x16(t_o + 16 * c, v);
+            tc05::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kv);
+            tc05::st_32x32b_x16(t_o + 16 * c, v);
+          }
         }
         tc05::wait_st();
         return true;
       };
-      // rows that have seen nothing yet take this tile's maximum first
-      const bool fresh = __any_sync(0xffffffffu, live && m == -INFINITY);
-      if (fresh || tile_vmax != vmax) {
-        if (!(ok = raise(fresh ? largest() : -INFINITY))) break;
-      }
-      // p' of the whole tile, in registers: no branch between its scores, so that their
-      // loads, exponentials and sums overlap. The running maximum is not looked for: a
-      // score that passes it by more than 6 or so shows in its group's sum, and the
-      // tile is done over.
-      uint32_t pk[kT / 2];
-      float sum, big;
+      // p' of 64 tokens at a time (16 where they are masked), over scores that are read
+      // already. The running maximum is not looked for: a score that passes it by more than
+      // 6 or so shows in its group's sum, and its step is done over. Rows that have seen
+      // nothing yet take the tile's maximum first. Without branches within a step, for its
+      // loads, exponentials and sums to mix, and rolled up, for the code to stay in the
+      // instruction cache beside the other warps': unrolled over the tile, fetches were the
+      // longest stall.
       // The special-function unit would take 2048 cycles of 256 rows' tile, as the products
-      // do; every fourth pair of exponentials goes to the multiply-add pipes instead.
-      auto group = [&](auto score, float f, int g, float m0, auto poly) {
-        const uint64_t f2 = pair(f, f), c2 = pair(lg[g] - m0, lg[g] - m0);
-        uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const uint64_t x2 = fma2(score(e), f2, c2), y2 = fma2(score(e + 2), f2, c2);
-          const float2 x = unpair(x2), y = unpair(y2);
-          const float2 p = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-          const float2 q = decltype(poly)::value && e % 8 == 4 ? exp2_poly(y2) : make_float2(exp2_fast(y.x), exp2_fast(y.y));
-          s0 = add2(s0, pair(p.x, p.y));
-          s1 = add2(s1, pair(q.x, q.y));
-          pk[8 * g + e / 2] = f16x2(p.x, p.y);
-          pk[8 * g + e / 2 + 1] = f16x2(q.x, q.y);
+      // do; every fourth pair of exponentials goes to the multiply-add pipes instead (which
+      // leave 2^-126 of what is masked).
+      bool seek = __any_sync(0xffffffffu, live && m == -INFINITY), rise = seek || tile_vmax != vmax;
+      int g0 = 0, seek_to = P::kGroups;
+      while (g0 < P::kGroups) {
+        if (rise) {
+          if (!(ok = raise(seek ? largest(g0, seek_to) : -INFINITY, 8 * g0))) break;
+          rise = false;
         }
-        const float2 t = unpair(add2(s0, s1));
-        big = fmaxf(big, t.x + t.y);
-        sum = fmaf(t.x + t.y, exp2_fast(-lg[g]), sum);
-      };
-      while (true) {
         const float m0 = m == -INFINITY ? 0.f : m;
-        sum = big = 0.f;
+        float part = 0.f, big = 0.f;
+        auto group = [&](const uint32_t* x, float f, int g, uint32_t* pk) {
+          const float lg = __shfl_sync(0xffffffffu, scale.y, g);
+          const uint64_t f2 = pair(f, f), c2 = pair(lg - m0, lg - m0);
+          uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const uint64_t x2 = fma2(pair(x[e], x[e + 1]), f2, c2), y2 = fma2(pair(x[e + 2], x[e + 3]), f2, c2);
+            const float2 y = unpair(y2), z = unpair(x2);
+            const float2 p = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+            const float2 q = e % 8 == 4 ? exp2_poly(y2) : make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            s0 = add2(s0, pair(p.x, p.y));
+            s1 = add2(s1, pair(q.x, q.y));
+            pk[e / 2] = f16x2(p.x, p.y);
+            pk[e / 2 + 1] = f16x2(q.x, q.y);
+          }
+          const float2 t = unpair(add2(s0, s1));
+          big = fmaxf(big, t.x + t.y);
+          part = fmaf(t.x + t.y, exp2_fast(-lg), part);
+        };
+        int step;
         if (!special) {
-          uint32_t v[2][32];
-          tc05::ld_32x32b_x32(t_s, v[0]);
+          step = 4;
+          uint32_t v[2][32], pk[32];
+          tc05::ld_32x32b_x32(t_s + 16 * g0, v[0]);
+          tc05::ld_32x32b_x32(t_s + 16 * g0 + 32, v[1]);
+          tc05::wait_ld();
 #pragma unroll
-          for (int c = 0; c < kT / 32; ++c) {
-            tc05::wait_ld();
-            if (c + 1 < kT / 32) tc05::ld_32x32b_x32(t_s + 32 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-              group([&](int e) { return pair(v[c & 1][16 * half + e], v[c & 1][16 * half + e + 1]); },
-                    fs[2 * c + half], 2 * c + half, m0, std::true_type{});
-          }
+          for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), factor(g0 + g), g0 + g, pk + 8 * g);
+          rise = __any_sync(0xffffffffu, big > 32768.f);
+          if (!rise) tc05::st_32x32b_x32(t_s + 8 * g0, pk);
         } else {
+          step = 1;
+          uint32_t v[16], pk[8];
+          tc05::ld_32x32b_x16(t_s + 16 * g0, v);
+          tc05::wait_ld();
+          const float f = factor(g0);
 #pragma unroll
-          for (int g = 0; g < P::kGroups; ++g) {
-            uint32_t v[16];
-            tc05::ld_32x32b_x16(t_s + 16 * g, v);
-            tc05::wait_ld();
-            float x[16], f = fs[g];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]);
-            masked_scores(x, g, f);
-            group([&](int e) { return pair(x[e], x[e + 1]); }, f, g, m0, std::false_type{});  // masked: exactly 0
-          }
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(masked(v[e], f, g0, e));
+          group(v, 1.f, g0, pk);
+          rise = __any_sync(0xffffffffu, big > 32768.f);
+          if (!rise) tc05::st_32x32b_x8(t_s + 8 * g0, pk);
         }
-        if (!__any_sync(0xffffffffu, big > 32768.f)) break;
-        if (!(ok = raise(largest()))) break;
+        if (rise) {
+          seek = true;
+          seek_to = g0 + step;
+        } else {
+          sum += part;
+          g0 += step;
+        }
       }
       if (!ok) break;
-      l += sum;
-#pragma unroll
-      for (int c = 0; c < kT / 64; ++c) {
-        uint32_t v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = pk[32 * c + e];
-        tc05::st_32x32b_x32(t_s + 32 * c, v);
-      }
+      if (m != -INFINITY) l += sum;
       tc05::wait_st();
       tc05::fence_before_sync();
       __syncwarp();
@@ -582,7 +577,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     if (any && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
     tc05::fence_after_sync();
     const float unit = vmax * 0x1p-8f;
-    if (w.whole) {
+    if (w.whole()) {
       const float inv = l > 0.f ? unit / l : (l == 0.f ? 0.f : l);
       uint16_t* op = a.out + grow * a.out_stride + int64_t(hq) * d;
 #pragma unroll
@@ -620,10 +615,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
                             __uint_as_float(v[4 * k + 3]) * unit);
       }
       if (w.t0 == 0 && tid == 0)  // the item goes on in the next CTAs
-        scr.open[cta] = Open{w.sq.r0, w.it.row0, w.at.h, w.it.rows, cut.part(B - 1 + (w.it.n - w.t1)) - cta + 1};
+        scr.open[cta] = Open{w.r0, w.row0, w.h, w.rows, cut.part(B - 1 + (w.n - w.t1)) - cta + 1};
     }
     tc05::fence_before_sync();
-    } while (w.next(a, limit));
+    }
   } else if (warp < P::kSoft + P::kConv) {
     // ------------------------------------------------------------ bytes to fp16
     fewer_registers<P::kConvRegs>();
@@ -636,16 +631,17 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const int c = (lane & 3) | (((lane >> 3) & (kWide - 1)) << 2);
     const int tk = ((lane >> 2) & 1) | ((lane >> (kWide == 1 ? 3 : kWide == 2 ? 4 : 5)) << 1);
     const int page = a.c.page, log2p = a.c.page_log2;
+    Piece w;
     // lane g < kGroups: the page of group g of a tile
     auto page_of = [&](int i) {
-      const int j = w.it.j0 + i * kT + 16 * lane;
-      return lane < P::kGroups && j < w.it.j1 && j + 16 > w.it.lo ? a.b.pages[int64_t(w.at.s) * a.b.max_pages + (j >> log2p)] : -1;
+      const int j = w.j0 + i * kT + 16 * lane;
+      return lane < P::kGroups && j < w.j1 && j + 16 > w.lo ? a.b.pages[int64_t(w.s) * a.b.max_pages + (j >> log2p)] : -1;
     };
     // checked where it is used, so that the load runs ahead
     auto checked = [&](int pid, int i) {
-      const int j = w.it.j0 + i * kT + 16 * lane;
+      const int j = w.j0 + i * kT + 16 * lane;
       if (pid >= 0 && pid < a.c.n_pages) return pid;
-      if (lane < P::kGroups && j < w.it.j1 && j + 16 > w.it.lo) atomicOr(a.err, kErrBounds);
+      if (lane < P::kGroups && j < w.j1 && j + 16 > w.lo) atomicOr(a.err, kErrBounds);
       return -1;
     };
     uint4 xk[kIt], xv[kIt];
@@ -653,8 +649,8 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const uint32_t mine = tk * d + 16 * c;
     auto fetch = [&](int i, int pid) {
       // where this lane's group starts in the cache (-1: nowhere)
-      const int64_t tl = int64_t(pid) * a.c.heads + w.at.h;
-      const int64_t group = pid < 0 ? -1 : (tl * page + ((w.it.j0 + i * kT + 16 * lane) & (page - 1))) * d;
+      const int64_t tl = int64_t(pid) * a.c.heads + w.h;
+      const int64_t group = pid < 0 ? -1 : (tl * page + ((w.j0 + i * kT + 16 * lane) & (page - 1))) * d;
       sc = make_float2(0.f, 0.f);
       if (pid >= 0) sc = make_float2(__ldg(a.c.k_scale + tl), __ldg(a.c.v_scale + tl));
 #pragma unroll
@@ -684,8 +680,8 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     };
     int tick = 0;
     bool ok = true;
-    do {
-    if (w.empty() || w.it.n == 0) continue;
+    for (int k = 0; ok && piece_of(k, w); ++k) {
+    if (w.n == 0) continue;
     float vmax = kTinyScale;
     int pid = checked(page_of(w.t0), w.t0);
     fetch(w.t0, pid);
@@ -704,9 +700,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         }
         const float lg = log2f(fmaxf(sc.y / vmax, 0x1p-60f)) + kPLog2;
         TileScales& ts = s_scales[tick % P::kSlots];
-        const int j = w.it.j0 + i * kT + 16 * lane;
-        if (lane < P::kGroups) reinterpret_cast<float2*>(ts.group)[lane] = make_float2(sc.x, lg);
-        const unsigned dead = __ballot_sync(0xffffffffu, lane < P::kGroups && j < w.it.j1 && pid < 0);
+        const int j = w.j0 + i * kT + 16 * lane;
+        if (lane < P::kGroups) ts.group[lane] = make_float2(sc.x, lg);
+        const unsigned dead = __ballot_sync(0xffffffffu, lane < P::kGroups && j < w.j1 && pid < 0);
         if (lane == 0) {
           ts.vmax = vmax;
           ts.dead = static_cast<int>(dead);
@@ -725,7 +721,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         if (i + 2 < w.t1) next = page_of(i + 2);
       }
     }
-    } while (ok && w.next(a, limit));
+    }
   } else {
     // ------------------------------------------------------------ products
     fewer_registers<P::kMmaRegs>();
@@ -768,8 +764,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     };
     bool ok = true;
     int tick = 0, pieces = 0;
-    do {
-      if (w.empty() || w.it.n == 0) continue;  // nothing, or rows that see no token
+    Piece w;
+    for (int k = 0; ok && piece_of(k, w); ++k) {
+      if (w.n == 0) continue;  // rows that see no token
       if (!(ok = wait1(&bar.q_full, pieces++ & 1))) break;
       const int n = w.t1 - w.t0;
       if constexpr (P::kMt == 2) {
@@ -810,10 +807,66 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           }
         }
       }
-    } while (ok && w.next(a, limit));
+    }
     // all products that this thread issued have finished before the CTA moves on
     commit(&bar.drain);
     if (!mbar_wait_bounded(&bar.drain, 0, 1000000000ull) && leader) atomicOr(a.err, kErrDrain);
+    } else if (warp == P::kSoft + P::kConv + 1) {
+    // ------------------------------------------------------------ the pieces of this range
+    Place at{};
+    int run = (__popc(__ballot_sync(0xffffffffu, s_pre[lane * kWarps] <= A)) - 1) * kWarps;
+    run += __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_pre[run + lane] <= A)) - 1;
+    int s = run * per;
+    int64_t off = A - s_pre[run];
+    while (true) {
+      const int64_t u = seq_units(s);
+      if (off < u) break;
+      off -= u;
+      ++s;
+    }
+    const Seq sq = load_seq(a.b, s, nullptr);
+    for (int first = item_rows<D>(a, sq, limit) - 1;; first -= 32) {
+      const int rt = first - lane;
+      const int units = rt >= 0 ? item_of<D>(a, sq, rt).units : 0;
+      int64_t upto = int64_t(units) * a.c.heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, off < upto);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        if (lane == src) {
+          const int64_t rest = off - (upto - int64_t(units) * a.c.heads);
+          at = Place{s, rt, static_cast<int>(rest / units), static_cast<int>(rest % units)};
+        }
+        at.s = __shfl_sync(0xffffffffu, at.s, src);
+        at.rt = __shfl_sync(0xffffffffu, at.rt, src);
+        at.h = __shfl_sync(0xffffffffu, at.h, src);
+        at.u0 = __shfl_sync(0xffffffffu, at.u0, src);
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    Walk<D> w;
+    w.start(a, at, B - A);
+    int k = 0;
+    auto publish = [&](int n) {
+      if (k >= 2 && !wait(&bar.plan_empty[k & 1], ((k >> 1) & 1) ^ 1, kErrWaitEmpty)) return false;
+      if (lane == 0) {
+        s_piece[k & 1] = Piece{w.at.s, w.at.h, w.sq.r0, w.it.row0, w.it.rows, w.sq.n * a.group, w.it.past, w.it.lo, w.it.j0, w.it.j1,
+                               n, w.t0, w.t1};
+        mbar_arrive(&bar.plan_full[k & 1]);
+      }
+      ++k;
+      return true;
+    };
+    bool ok = true;
+    do {
+      if (!w.empty()) ok = publish(w.it.n);
+    } while (ok && w.next(a, limit));
+    if (ok) publish(-1);
     }
   }
   __syncthreads();
