@@ -564,8 +564,8 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
   if (tid < 2 * kWarps) s_piece[tid].rows = 0;
   if (tid == 0) prefetch_tmap(&map_k), prefetch_tmap(&map_v);
   fence_mbar_init();
-  pdl_launch_dependents();
   pdl_wait_primary();
+  pdl_launch_dependents();  // not before: kv_prompt_kernel relies on it
   // ---- tiles before each run of sequences
   const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
   int64_t mine = 0;
@@ -686,44 +686,13 @@ kv_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap map_k, 
   }
 }
 
-// Joins the items that several CTAs shared: one CTA for each row of an item that
-// an attention CTA's range ends within. Its warps take a run of the pieces each.
-constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 kv_join_kernel(const AttendArgs a, const Scratch sc) {
-  constexpr int kCols = Joined<D>::kCols;
-  __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ JoinShared<D> shared;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int c = blockIdx.x, lr = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Open p = sc.open[c];
-  if (lr >= p.rows) return;
-  const int run = (p.n + kJoinWarps - 1) / kJoinWarps, first = warp * run;
-  Joined<D> r;
-  join_row<D>(sc.rows, a.c.d, lr, min(run, p.n - first),
-              [&](int k) { return sc.joined + int64_t(2 * (c + first + k) + (first + k == 0 ? 1 : 0)) * sc.slot_floats; }, r);
-  if (warp > 0) {
-    if (lane == 0) s_m[warp] = r.m, s_l[warp] = r.l;
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) s_o[warp][lane + 32 * i] = r.o[i];
-  }
-  __syncthreads();
-  if (warp > 0) return;
-  float top = r.m;
-  for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, s_m[k]);
-  const float to = top == -INFINITY ? 0.f : top, keep = exp2_fast(r.m - to);
-  r.m = top;
-  r.l *= keep;
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) r.o[i] *= keep;
-  for (int k = 1; k < kJoinWarps; ++k) {
-    const float w = exp2_fast(s_m[k] - to);
-    r.l = fmaf(s_l[k], w, r.l);
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(s_o[k][lane + 32 * i], w, r.o[i]);
-  }
-  write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
+  join_open<D>(a, sc, sc.open[blockIdx.x], blockIdx.x, blockIdx.y, shared);
 }
 
 int padded(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -766,14 +735,13 @@ cudaError_t launch_shape(const AttendArgs& a, int limit, cudaStream_t stream, in
     return e;
   Scratch sc;
   scratch_shape<D, NR>(a.c, a.b, a.group, sms, &sc, a.scratch);
-  const int64_t rows = int64_t(a.b.max_new) * a.group;
   const uint64_t wait = wait_limit_ns();
   if ((e = launch_pdl(kv_attend_kernel<D, NR>, dim3(sms), dim3(S::kThreads), S::kSmem, stream, a, mk, mv, sc, limit, wait)) !=
       cudaSuccess)
     return e;
-  e = launch_pdl(kv_join_kernel<D>, dim3(sms, sc.rows), dim3(kJoinWarps * 32), 0, stream, a, sc);
-  if (e != cudaSuccess || rows <= limit) return e;
-  return launch_kv_prompt(a, limit, a.scratch + scratch_shape<D, NR>(a.c, a.b, a.group, sms), stream, sms);
+  if (int64_t(a.b.max_new) * a.group > limit)  // it joins this kernel's rows too
+    return launch_kv_prompt(a, limit, sc, a.scratch + scratch_shape<D, NR>(a.c, a.b, a.group, sms), stream, sms);
+  return launch_pdl(kv_join_kernel<D>, dim3(sms, sc.rows), dim3(kJoinWarps * 32), 0, stream, a, sc);
 }
 
 }  // namespace

@@ -92,9 +92,11 @@ cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream);
 size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
 // Sequences with more than `limit` rows (query tokens times heads of a group).
+// Launched directly behind kv_attend_kernel, whose shared rows (`few`) it joins with its own.
 // `scratch`: kv_prompt_scratch bytes.
+struct Scratch;
 size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
-cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms);
+cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms);
 cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms);
 
 #ifdef __CUDACC__

@@ -169,6 +169,45 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, const RowOut& ro,
 }
 
 
+// Joins row lr of an item that several CTAs shared, from CTA c on; the CTA's warps take a run
+// of its pieces each.
+constexpr int kJoinWarps = 4;
+template <int D>
+struct JoinShared {
+  float o[kJoinWarps][D], m[kJoinWarps], l[kJoinWarps];
+};
+template <int D>
+__device__ __forceinline__ void join_open(const AttendArgs& a, const Scratch& sc, const Open& p, int c, int lr, JoinShared<D>& sh) {
+  constexpr int kCols = Joined<D>::kCols;
+  if (lr >= p.rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = (p.n + kJoinWarps - 1) / kJoinWarps, first = warp * run;
+  Joined<D> r;
+  join_row<D>(sc.rows, a.c.d, lr, min(run, p.n - first),
+              [&](int k) { return sc.joined + int64_t(2 * (c + first + k) + (first + k == 0 ? 1 : 0)) * sc.slot_floats; }, r);
+  if (warp > 0) {
+    if (lane == 0) sh.m[warp] = r.m, sh.l[warp] = r.l;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) sh.o[warp][lane + 32 * i] = r.o[i];
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  float top = r.m;
+  for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, sh.m[k]);
+  const float to = top == -INFINITY ? 0.f : top, keep = exp2_fast(r.m - to);
+  r.m = top;
+  r.l *= keep;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) r.o[i] *= keep;
+  for (int k = 1; k < kJoinWarps; ++k) {
+    const float w = exp2_fast(sh.m[k] - to);
+    r.l = fmaf(sh.l[k], w, r.l);
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) r.o[i] = fmaf(sh.o[k][lane + 32 * i], w, r.o[i]);
+  }
+  write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
+}
+
 inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 }  // namespace mq

@@ -98,6 +98,11 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
 // True in one lane of the (converged) warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -135,7 +140,7 @@ struct Plan {
   static constexpr int kStart = D == 256 ? 6 : 3;
 };
 
-struct TileScales {
+struct alignas(16) TileScales {
   float2 group[8];  // K scale, log2 of V's factor
   float vmax;
   int dead;         // a bit for each group that may not be read
@@ -274,7 +279,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     fence_mbar_init();
   }
   pdl_launch_dependents();
-  pdl_wait_primary();
+  // This kernel follows kv_attend_kernel, which starts its dependents only when what came
+  // before it is complete: so this one may begin at once, beside it, and waits for it at its
+  // end, for the next kernel's sake.
   // ---- units before each run of sequences: a warp sums a run
   const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
   auto seq_units = [&](int s) {  // of one sequence, by the warp
@@ -315,7 +322,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   const int cta = blockIdx.x;
   const int ctas = static_cast<int>(min(int64_t(gridDim.x), max((total + P::kStart) / (P::kStart + 1), int64_t(1))));
   if (tid == 0) scr.open[cta].rows = 0;
-  if (cta >= ctas || total == 0) return;
+  if (cta >= ctas || total == 0) {
+    pdl_wait_primary();
+    return;
+  }
   const Cut cut(total, ctas);
   const int64_t A = cut.first(cta), B = cut.first(cta + 1);
   if (warp == P::kSoft + P::kConv) {
@@ -356,6 +366,13 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     bool ok = true;
     int tick = 0;  // tiles of this CTA before
+    // Rows go to and from global memory with neighbouring lanes on one row (a lane a row would
+    // touch 32 lines an instruction): lane = row sub, 16-byte chunk `chunk`.
+    constexpr int kLanesRow = D / 8, kRowsAt = 32 / kLanesRow, kLoads = 32 / kRowsAt;
+    const int sub = lane / kLanesRow, chunk = lane % kLanesRow;
+    auto row_chunk = [&](int row, int c) {  // of this warp's 32 rows, in the queries' shared memory
+      return sq_base + (mt * P::kBlocks + (c >> 3)) * P::kQBlock + (32 * (warp & 3) + row) * 128 + (((c & 7) ^ (row & 7)) << 4);
+    };
     Piece w;
     for (int k = 0; piece_of(k, w); ++k) {
     const bool live = lr < w.rows;
@@ -363,41 +380,36 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const int64_t grow = int64_t(w.r0) + qi;
     const int place = live ? w.past + qi : -1;
     float fac = 0.f;
-    if (w.n > 0) {  // this thread's query, scaled by a power of two to below 2
-      const uint4* qp = reinterpret_cast<const uint4*>(a.q + grow * a.q_stride + int64_t(hq) * d);
-      constexpr int kAll = D / 8, kBatch = kAll < 16 ? kAll : 16;  // loads on their way at once
-      uint4 u[kBatch];
-      auto load = [&](int c0) {
+    if (w.n > 0) {  // this warp's queries, each row scaled by a power of two to below 2
+      const int64_t from = live ? grow * a.q_stride + int64_t(hq) * d : -1;
+      constexpr int kBatch = kLoads < 16 ? kLoads : 16;  // loads on their way at once
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) u[c] = live && c0 + c < 2 * chunks ? __ldg(qp + c0 + c) : make_uint4(0, 0, 0, 0);
-      };
-      float mx = 0.f;
+      for (int k0 = 0; k0 < kLoads; k0 += kBatch) {
+        uint4 u[kBatch];
 #pragma unroll
-      for (int c0 = kAll - kBatch; c0 >= 0; c0 -= kBatch) {
-        load(c0);
+        for (int k = 0; k < kBatch; ++k) {
+          const int64_t at = __shfl_sync(0xffffffffu, from, (k0 + k) * kRowsAt + sub);
+          u[k] = at >= 0 && chunk < 2 * chunks ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + chunk) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
-          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+        for (int k = 0; k < kBatch; ++k) {
+          const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+          float mx = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-        }
-      }
-      int ex = __float_as_int(mx) >> 23;
-      ex = ex < 1 || ex > 253 ? 127 : ex;
-      const float down = __int_as_float((254 - ex) << 23) * (a.scale < 0.f ? -1.f : 1.f);
-      fac = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
 #pragma unroll
-      for (int c0 = 0; c0 < kAll; c0 += kBatch) {
-        if (c0 > 0) load(c0);
+          for (int o = kLanesRow / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          int ex = __float_as_int(mx) >> 23;
+          ex = ex < 1 || ex > 253 ? 127 : ex;
+          const float down = __int_as_float((254 - ex) << 23) * (a.scale < 0.f ? -1.f : 1.f);
+          const float up = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
+          const float mine = __shfl_sync(0xffffffffu, up, (lane % kRowsAt) * kLanesRow);
+          if (lane / kRowsAt == k0 + k) fac = mine;
+          uint32_t y[4];
 #pragma unroll
-        for (int c = 0; c < kBatch; ++c) {
-          const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
-          uint32_t x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xFFFF0000u) * down);
-          const int at = c0 + c;
-          sts128(sq_base + (mt * P::kBlocks + (at >> 3)) * P::kQBlock + r * 128 + (((at & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
+          for (int i = 0; i < 4; ++i) y[i] = f16x2(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xFFFF0000u) * down);
+          sts128(row_chunk((k0 + k) * kRowsAt + sub, chunk), y[0], y[1], y[2], y[3]);
         }
       }
       fence_async_smem();
@@ -409,16 +421,19 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     const int w_lo = w.past + first_row / a.group, w_hi = w.past + min(first_row + 31, w.all - 1) / a.group;
     const bool ragged = w.row0 + 128 * mt + 128 > w.all || a.softcap > 0.f;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
-    // A tile's scales, lane g group g's, taken while its scores are still being made: the
-    // products keep shared memory busy, and a load waits for hundreds of cycles.
-    float2 scale = make_float2(0.f, 0.f);
-    float tile_vmax = 0.f;
+    // A tile's scales (K's times this row's factor), taken while its scores are still being
+    // made: the products keep shared memory busy, and a load waits for hundreds of cycles.
+    float fs[P::kGroups], lg[P::kGroups], tile_vmax = 0.f;
     int dead = 0;
     auto take = [&](int tick) {
       const int slot = tick % P::kSlots;
       if (!wait(&bar.sc_full[slot], (tick / P::kSlots) & 1, kErrWaitFull)) return false;
       const TileScales& ts = s_scales[slot];
-      if (lane < P::kGroups) scale = ts.group[lane];
+#pragma unroll
+      for (int g = 0; g < P::kGroups; g += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(ts.group + g);
+        fs[g] = fac * x.x, lg[g] = x.y, fs[g + 1] = fac * x.z, lg[g + 1] = x.w;
+      }
       tile_vmax = ts.vmax;
       dead = ts.dead;
       return true;
@@ -431,24 +446,41 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       const uint32_t t_s = tmem + lanes + slot * kT;
       const int jt = w.j0 + i * kT;
       const bool special = ragged || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
-      auto factor = [&](int g) { return fac * __shfl_sync(0xffffffffu, scale.x, g); };
-      // A score of group g, scaled, capped and masked (where some row of the warp needs it).
-      auto masked = [&](uint32_t v, float f, int g, int e) {
-        float y = __uint_as_float(v) * f;
-        if (a.softcap > 0.f) y = cap_out * tanh_fast(y * cap_in);
-        const int j = jt + 16 * g + e;
-        return j > place || (a.window > 0 && j <= place - a.window) || ((dead >> g) & 1) ? -INFINITY : y;
+      const float2* group_scales = s_scales[tick % P::kSlots].group;
+      auto factor = [&](int g) { return fac * group_scales[g].x; };
+      // The scores of groups g, g + 1, scaled, and where some row of the warp needs it capped and masked.
+      auto scores = [&](uint32_t (&v)[32], int g) {
+        tc05::ld_32x32b_x32(t_s + 16 * g, v);
+        const float f0 = factor(g), f1 = factor(g + 1);
+        tc05::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * (e < 16 ? f0 : f1));
+        if (a.softcap > 0.f) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(cap_out * tanh_fast(__uint_as_float(v[e]) * cap_in));
+        }
+        if (special) {
+          const int hi = place - jt - 16 * g, low = a.window > 0 ? hi - a.window : -1;
+          const int hi0 = (dead >> g) & 1 ? -1 : hi, hi1 = (dead >> g) & 2 ? -1 : hi;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e > (e < 16 ? hi0 : hi1) || e <= low) v[e] = __float_as_uint(-INFINITY);
+        }
       };
-      auto largest = [&](int g0, int g1) {  // score of groups g0 .. g1 - 1
+      // The largest of groups g .. end - 1, or of as many as it takes for each row to see one.
+      auto largest = [&](int g, int end, bool enough) {
         float top = -INFINITY;
 #pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
-          uint32_t v[16];
-          tc05::ld_32x32b_x16(t_s + 16 * g, v);
-          tc05::wait_ld();
-          const float f = factor(g);
+        for (; g < end; g += 2) {
+          uint32_t v[32];
+          scores(v, g);
+          float t[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, special ? masked(v[e], f, g, e) : __uint_as_float(v[e]) * f);
+          for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(v[e]);
+#pragma unroll
+          for (int e = 4; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(v[e]));
+          top = fmaxf(top, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+          if (enough && __all_sync(0xffffffffu, !live || top > -INFINITY)) break;
         }
         return top;
       };
@@ -491,10 +523,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         tc05::wait_st();
         return true;
       };
-      // p' of 64 tokens at a time (16 where they are masked), over scores that are read
+      // p' of 64 tokens at a time (32 where they are masked), over scores that are read
       // already. The running maximum is not looked for: a score that passes it by more than
       // 6 or so shows in its group's sum, and its step is done over. Rows that have seen
-      // nothing yet take the tile's maximum first. Without branches within a step, for its
+      // nothing yet take a maximum first, of the tokens up to the first they see. Without branches within a step, for its
       // loads, exponentials and sums to mix, and rolled up, for the code to stay in the
       // instruction cache beside the other warps': unrolled over the tile, fetches were the
       // longest stall.
@@ -502,16 +534,16 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // do; every fourth pair of exponentials goes to the multiply-add pipes instead (which
       // leave 2^-126 of what is masked).
       bool seek = __any_sync(0xffffffffu, live && m == -INFINITY), rise = seek || tile_vmax != vmax;
+      bool enough = true;
       int g0 = 0, seek_to = P::kGroups;
       while (g0 < P::kGroups) {
         if (rise) {
-          if (!(ok = raise(seek ? largest(g0, seek_to) : -INFINITY, 8 * g0))) break;
-          rise = false;
+          if (!(ok = raise(seek ? largest(g0, seek_to, enough) : -INFINITY, 8 * g0))) break;
+          rise = enough = false;
         }
         const float m0 = m == -INFINITY ? 0.f : m;
         float part = 0.f, big = 0.f;
-        auto group = [&](const uint32_t* x, float f, int g, uint32_t* pk) {
-          const float lg = __shfl_sync(0xffffffffu, scale.y, g);
+        auto group = [&](const uint32_t* x, float f, float lg, uint32_t* pk) {
           const uint64_t f2 = pair(f, f), c2 = pair(lg - m0, lg - m0);
           uint64_t s0 = 0, s1 = 0;
 #pragma unroll
@@ -537,20 +569,17 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           tc05::ld_32x32b_x32(t_s + 16 * g0 + 32, v[1]);
           tc05::wait_ld();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), factor(g0 + g), g0 + g, pk + 8 * g);
+          for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), fs[g], lg[g], pk + 8 * g);
           rise = __any_sync(0xffffffffu, big > 32768.f);
           if (!rise) tc05::st_32x32b_x32(t_s + 8 * g0, pk);
         } else {
-          step = 1;
-          uint32_t v[16], pk[8];
-          tc05::ld_32x32b_x16(t_s + 16 * g0, v);
-          tc05::wait_ld();
-          const float f = factor(g0);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(masked(v[e], f, g0, e));
-          group(v, 1.f, g0, pk);
+          step = 2;
+          uint32_t v[32], pk[16];
+          scores(v, g0);
+          group(v, 1.f, group_scales[g0].y, pk);
+          group(v + 16, 1.f, group_scales[g0 + 1].y, pk + 8);
           rise = __any_sync(0xffffffffu, big > 32768.f);
-          if (!rise) tc05::st_32x32b_x8(t_s + 8 * g0, pk);
+          if (!rise) tc05::st_32x32b_x16(t_s + 8 * g0, pk);
         }
         if (rise) {
           seek = true;
@@ -558,6 +587,8 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         } else {
           sum += part;
           g0 += step;
+#pragma unroll
+          for (int g = 0; g + 4 < P::kGroups; ++g) fs[g] = fs[g + 4], lg[g] = lg[g + 4];  // the next whole step's
         }
       }
       if (!ok) break;
@@ -576,10 +607,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     if (P::kMt == 1 && w.t1 - w.t0 > 1 && !(ok = wait(&bar.o_done[mt], tick & 1, kErrMma))) break;
     if (any && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
     tc05::fence_after_sync();
+    // (through the queries' shared memory, which no product reads any more)
     const float unit = vmax * 0x1p-8f;
     if (w.whole()) {
       const float inv = l > 0.f ? unit / l : (l == 0.f ? 0.f : l);
-      uint16_t* op = a.out + grow * a.out_stride + int64_t(hq) * d;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32] = {};
@@ -595,29 +626,51 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
             const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(v[8 * k + 2 * e]) * inv, __uint_as_float(v[8 * k + 2 * e + 1]) * inv);
             x[e] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          if (live && 2 * c + k / 2 < chunks) *reinterpret_cast<uint4*>(op + 32 * c + 8 * k) = make_uint4(x[0], x[1], x[2], x[3]);
+          sts128(row_chunk(lane, 4 * c + k), x[0], x[1], x[2], x[3]);
         }
+      }
+      __syncwarp();
+      const int64_t to = live ? grow * a.out_stride + int64_t(hq) * d : -1;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int64_t at = __shfl_sync(0xffffffffu, to, k * kRowsAt + sub);
+        const uint4 x = lds128(row_chunk(k * kRowsAt + sub, chunk));
+        if (at >= 0 && chunk < 2 * chunks) reinterpret_cast<uint4*>(a.out + at)[chunk] = x;
       }
       if (a.lse && live) a.lse[grow * (a.c.heads * a.group) + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     } else {
       float* part = scr.joined + int64_t(2 * cta + (w.t0 > 0 ? 0 : 1)) * scr.slot_floats;
       if (live) *reinterpret_cast<float2*>(part + scr.rows * d + 2 * lr) = make_float2(m, l);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // D / 2 columns: as many bytes as a row of queries
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t v[32];
-        tc05::ld_32x32b_x32(t_o + 32 * c, v);
-        tc05::wait_ld();
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t v[32];
+          tc05::ld_32x32b_x32(t_o + half * (D / 2) + 32 * c, v);
+          tc05::wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (live && 2 * c + k / 4 < chunks)
-            *reinterpret_cast<float4*>(part + int64_t(lr) * d + 32 * c + 4 * k) =
-                make_float4(__uint_as_float(v[4 * k]) * unit, __uint_as_float(v[4 * k + 1]) * unit, __uint_as_float(v[4 * k + 2]) * unit,
-                            __uint_as_float(v[4 * k + 3]) * unit);
+          for (int k = 0; k < 8; ++k) {
+            uint32_t x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __float_as_uint(__uint_as_float(v[4 * k + e]) * unit);
+            sts128(row_chunk(lane, 8 * c + k), x[0], x[1], x[2], x[3]);
+          }
+        }
+        __syncwarp();
+        const int col = half * (D / 2) + 4 * chunk, first = 128 * mt + 32 * (warp & 3);
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int row = k * kRowsAt + sub;
+          const uint4 x = lds128(row_chunk(row, chunk));
+          if (first + row < w.rows && col < d) *reinterpret_cast<uint4*>(part + int64_t(first + row) * d + col) = x;
+        }
+        __syncwarp();
       }
       if (w.t0 == 0 && tid == 0)  // the item goes on in the next CTAs
         scr.open[cta] = Open{w.r0, w.row0, w.h, w.rows, cut.part(B - 1 + (w.n - w.t1)) - cta + 1};
     }
     tc05::fence_before_sync();
+    __syncwarp();
     }
   } else if (warp < P::kSoft + P::kConv) {
     // ------------------------------------------------------------ bytes to fp16
@@ -874,18 +927,25 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     tc05::fence_after_sync();
     tc05::dealloc(tmem, 512);
   }
+  pdl_wait_primary();
 }
 
-// Joins the items that several CTAs shared, a warp a row.
-constexpr int kJoinWarps = 4;
+// Joins what several CTAs shared: blocks y < kJoinShare a share of the rows of a prompt's
+// item, a warp a row; the others a row of kv_attend_kernel's.
+constexpr int kJoinShare = 16;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-kv_prompt_join_kernel(const AttendArgs a, const Scratch sc) {
+kv_prompt_join_kernel(const AttendArgs a, const Scratch sc, const Scratch few) {
+  __shared__ JoinShared<D> shared;
   pdl_launch_dependents();
   pdl_wait_primary();
   const int c = blockIdx.x;
+  if (blockIdx.y >= kJoinShare) {
+    join_open<D>(a, few, few.open[c], c, blockIdx.y - kJoinShare, shared);
+    return;
+  }
   const Open p = sc.open[c];
-  for (int lr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); lr < p.rows; lr += gridDim.y * kJoinWarps) {
+  for (int lr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); lr < p.rows; lr += kJoinShare * kJoinWarps) {
     Joined<D> r;
     join_row<D>(sc.rows, a.c.d, lr, p.n, [&](int k) { return sc.joined + int64_t(2 * (c + k) + (k == 0 ? 1 : 0)) * sc.slot_floats; }, r);
     write_row<D>(a, row_out(a, p.r0, p.h, p.first_row + lr), r);
@@ -901,7 +961,7 @@ size_t layout(const KvCache& c, const KvBatch& b, int group, int sms, Scratch* s
 }
 
 template <int D>
-cudaError_t launch(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms) {
+cudaError_t launch(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms) {
   using P = Plan<D>;
   cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
@@ -909,7 +969,7 @@ cudaError_t launch(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_
   layout<D>(a.c, a.b, a.group, sms, &sc, scratch);
   e = launch_pdl(kv_prompt_kernel<D>, dim3(sms), dim3(P::kThreads), P::kSmem, stream, a, sc, limit, wait_limit_ns());
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_prompt_join_kernel<D>, dim3(sms, 16), dim3(kJoinWarps * 32), 0, stream, a, sc);
+  return launch_pdl(kv_prompt_join_kernel<D>, dim3(sms, kJoinShare + few.rows), dim3(kJoinWarps * 32), 0, stream, a, sc, few);
 }
 
 }  // namespace
@@ -918,10 +978,10 @@ size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms)
   return c.d <= 64 ? layout<64>(c, b, group, sms) : c.d <= 128 ? layout<128>(c, b, group, sms) : layout<256>(c, b, group, sms);
 }
 
-cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, uint8_t* scratch, cudaStream_t stream, int sms) {
-  if (a.c.d <= 64) return launch<64>(a, limit, scratch, stream, sms);
-  if (a.c.d <= 128) return launch<128>(a, limit, scratch, stream, sms);
-  return launch<256>(a, limit, scratch, stream, sms);
+cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms) {
+  if (a.c.d <= 64) return launch<64>(a, limit, few, scratch, stream, sms);
+  if (a.c.d <= 128) return launch<128>(a, limit, few, scratch, stream, sms);
+  return launch<256>(a, limit, few, scratch, stream, sms);
 }
 
 }  // namespace mq
