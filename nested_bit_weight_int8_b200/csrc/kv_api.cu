@@ -206,7 +206,7 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
   a.n_q_heads = static_cast<int>(n_q_heads);
   cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
-  return finish(launch_kv_append(a, dtype, static_cast<cudaStream_t>(stream)), who);
+  return finish(launch_kv_append(a, dtype, static_cast<cudaStream_t>(stream), sm_count()), who);
 }
 
 mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const int32_t* first, const int32_t* out_start,

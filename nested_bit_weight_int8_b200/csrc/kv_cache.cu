@@ -221,10 +221,15 @@ __device__ __forceinline__ uint32_t code_of(float x, float scale) {
 
 constexpr int kUnitsPerThread = 4;
 
+constexpr int kHeadsPerThread = 4;
+
 // CTAs below kv_blocks: one page of one sequence, one head, K or V. The new
 // values of the page stay in registers (at most 4 units of 8 a thread) from
 // the maximum to the bytes, so they are read once. The others: the queries,
-// one row and a share of its heads each.
+// one row and a share of its heads each, up to 4 a thread. Bound by the bytes; what
+// costs is the chain of loads that a short CTA waits for (lengths, page, scale,
+// values), so each load starts as soon as its address is known: values before the
+// page and its scale, queries before the search for their sequence.
 template <typename T>
 __global__ void __launch_bounds__(1024)
 kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits) {
@@ -236,34 +241,52 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
   if (static_cast<int>(blockIdx.x) >= kv_blocks) {
     const int i = blockIdx.x - kv_blocks;
     const int row = i / q_splits;
-    int pos = 0;
-    if (a.rope.turns) {
-      if (a.positions) {
-        pos = a.positions[row];
-        if (row >= a.b.row_start[a.b.n_seqs]) return;
-      } else {
-        const int s = find_seq(a.b, row, lane);
-        if (s < 0) return;
-        pos = a.b.kv_len[s] - a.b.row_start[s + 1] + row;
-      }
-    } else if (row >= a.b.row_start[a.b.n_seqs]) {
-      return;
-    }
-    const int head_lanes = blockDim.x / units;
+    const int head_lanes = blockDim.x / units, stride = q_splits * head_lanes;
     const int u = tid % units, hl = tid / units;
-    if (hl >= head_lanes) return;
     const Unit un = unit_of<4>(u, a.rope.turns ? a.rope.rot : 0, il);
+    const T* x = static_cast<const T*>(a.q) + row * a.q_stride;
+    float p[kHeadsPerThread][4], q[kHeadsPerThread][4];
+    const int h0 = (i % q_splits) * head_lanes + hl;
+#pragma unroll
+    for (int k = 0; k < kHeadsPerThread; ++k) {
+      const int h = h0 + k * stride;
+      if (hl < head_lanes && h < a.n_q_heads) {
+        load_v<T, 4>(x + int64_t(h) * d + un.c0, p[k]);
+        load_v<T, 4>(x + int64_t(h) * d + un.c1, q[k]);
+      }
+    }
+    uint64_t turns[4];
+    if (un.turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) turns[e] = a.rope.turns[u * 4 + e];
+    }
+    int pos = 0;
+    if (a.rope.turns && !a.positions) {
+      const int s = find_seq(a.b, row, lane);
+      if (s < 0) return;
+      pos = a.b.kv_len[s] - a.b.row_start[s + 1] + row;
+    } else {
+      if (a.rope.turns) pos = a.positions[row];
+      if (row >= a.b.row_start[a.b.n_seqs]) return;
+    }
+    if (hl >= head_lanes) return;
     float sn[4], cs[4];
-    if (un.turned) unit_angles<4>(a.rope, u, pos, sn, cs);
-    for (int h = (i % q_splits) * head_lanes + hl; h < a.n_q_heads; h += q_splits * head_lanes) {
-      const T* x = static_cast<const T*>(a.q) + row * a.q_stride + int64_t(h) * d;
-      float p[4], q[4];
-      load_v<T, 4>(x + un.c0, p);
-      load_v<T, 4>(x + un.c1, q);
-      if (un.turned) unit_turn<4>(il, p, q, sn, cs);
+    if (un.turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        turn_sincos(turns[e] * static_cast<uint64_t>(static_cast<int64_t>(pos)), sn[e], cs[e]);
+        sn[e] *= a.rope.factor;
+        cs[e] *= a.rope.factor;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kHeadsPerThread; ++k) {
+      const int h = h0 + k * stride;
+      if (h >= a.n_q_heads) break;
+      if (un.turned) unit_turn<4>(il, p[k], q[k], sn, cs);
       __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.q_out) + (int64_t(row) * a.n_q_heads + h) * d;
-      store_v<__nv_bfloat16, 4>(o + un.c0, p);
-      store_v<__nv_bfloat16, 4>(o + un.c1, q);
+      store_v<__nv_bfloat16, 4>(o + un.c0, p[k]);
+      store_v<__nv_bfloat16, 4>(o + un.c1, q[k]);
     }
     return;
   }
@@ -280,33 +303,38 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
   const int base = index << a.c.page_log2;
   if (sq.n == 0 || base >= sq.len) return;
   const int lo = max(start - base, 0), hi = min(sq.len - base, a.c.page);  // new tokens of the page
+  // row of the page's token t: r0 + (base + t) - (len - n)
+  const int64_t row0 = sq.r0 + int64_t(base) - (sq.len - sq.n);
+  const T* x = static_cast<const T*>(is_v ? a.v : a.k) + int64_t(h) * d;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const bool turn = a.rope.turns && !is_v;
+  const int total = (hi - lo) * units;
+  float va[kUnitsPerThread][4], vb[kUnitsPerThread][4];
+#pragma unroll
+  for (int k = 0; k < kUnitsPerThread; ++k) {
+    const int w = tid + k * blockDim.x;
+    if (w < total) {
+      const Unit un = unit_of<4>(w % units, turn ? a.rope.rot : 0, il);
+      const T* xr = x + (row0 + lo + w / units) * stride;
+      load_v<T, 4>(xr + un.c0, va[k]);
+      load_v<T, 4>(xr + un.c1, vb[k]);
+    }
+  }
   const int pid = load_page(a.c, a.b, s, index, a.err);
   if (pid < 0) return;
   const int64_t tile = int64_t(pid) * a.c.heads + h;
   float* scale_p = (is_v ? a.c.v_scale : a.c.k_scale) + tile;
   uint8_t* codes = (is_v ? a.c.v : a.c.k) + tile * a.c.page * d;
   const float old = lo > 0 ? *scale_p : 0.f;
-  // row of the page's token t: r0 + (base + t) - (len - n)
-  const int64_t row0 = sq.r0 + int64_t(base) - (sq.len - sq.n);
-  const T* x = static_cast<const T*>(is_v ? a.v : a.k);
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const bool turn = a.rope.turns && !is_v;
-  const int total = (hi - lo) * units;
-  float va[kUnitsPerThread][4], vb[kUnitsPerThread][4];
   float mx = 0.f;
 #pragma unroll
   for (int k = 0; k < kUnitsPerThread; ++k) {
     const int w = tid + k * blockDim.x;
     if (w < total) {
       const int u = w % units;
-      const int64_t row = row0 + lo + w / units;
-      const Unit un = unit_of<4>(u, turn ? a.rope.rot : 0, il);
-      const T* xr = x + row * stride + int64_t(h) * d;
-      load_v<T, 4>(xr + un.c0, va[k]);
-      load_v<T, 4>(xr + un.c1, vb[k]);
-      if (un.turned) {
+      if (unit_of<4>(u, turn ? a.rope.rot : 0, il).turned) {
         float sn[4], cs[4];
-        const int pos = a.positions ? a.positions[row] : base + lo + w / units;
+        const int pos = a.positions ? a.positions[row0 + lo + w / units] : base + lo + w / units;
         unit_angles<4>(a.rope, u, pos, sn, cs);
         unit_turn<4>(il, va[k], vb[k], sn, cs);
       }
@@ -433,7 +461,7 @@ cudaError_t launch_rope(const void* x, int x_dtype, int64_t rows, int heads, int
   return rope_typed<__nv_bfloat16, __nv_bfloat16>(x, rows, heads, d, x_stride, positions, rope, y, y_stride, stream, sms);
 }
 
-cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream) {
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream, int sms) {
   const int units = a.c.d / 8;
   const int tokens = a.b.max_new < a.c.page ? a.b.max_new : a.c.page;
   int threads = 32;  // every unit of a page in registers: at most 4 a thread
@@ -442,8 +470,11 @@ cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream
   const int64_t kv_blocks = int64_t(a.b.n_seqs) * page_slots * a.c.heads * 2;
   int q_splits = 0;
   if (a.q) {
+    // a head a thread where rows are few (latency), else up to 4 (bytes on their way, and the
+    // row's sequence and cosines found once for them)
     const int head_lanes = threads / units;  // d <= 256: at most 32 units
-    q_splits = (a.n_q_heads + head_lanes - 1) / head_lanes;
+    const int most = (a.n_q_heads + head_lanes - 1) / head_lanes, least = (most + kHeadsPerThread - 1) / kHeadsPerThread;
+    q_splits = int64_t(a.b.n_rows) * least >= 4 * sms ? least : most;
   }
   const int64_t grid = kv_blocks + int64_t(a.b.n_rows) * q_splits;
   if (grid > 0x7fffffff) return cudaErrorNotSupported;

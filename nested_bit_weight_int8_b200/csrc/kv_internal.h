@@ -88,7 +88,7 @@ struct AttendArgs {
 cudaError_t launch_rope(const void* x, int x_dtype, int64_t rows, int heads, int d, int64_t x_stride,
                         const int32_t* positions, const Rope& rope, void* y, int y_dtype, int64_t y_stride,
                         cudaStream_t stream, int sms);
-cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream, int sms);
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream);
 size_t kv_attention_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
 // Sequences with more than `limit` rows (query tokens times heads of a group).
