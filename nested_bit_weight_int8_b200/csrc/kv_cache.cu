@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mq.h"
 #include "kv_internal.h"
@@ -235,16 +236,18 @@ struct Coder {
     r = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
     tiny = scale > 0.f && scale < 0x1p-100f;
   }
-  __device__ __forceinline__ uint32_t operator()(float x) const {
+  // TINY: the scale lies below 2^-100
+  template <bool TINY>
+  __device__ __forceinline__ uint32_t one(float x) const {
     float q = x * r;
-    q = tiny ? __fdiv_rn(x, s) : fmaf(fmaf(-q, s, x), r, q);
+    q = TINY ? __fdiv_rn(x, s) : fmaf(fmaf(-q, s, x), r, q);
     return __float_as_uint(q + 12583040.f);  // 1.5 2^23 + 128: rounds to an integer, ties to even
   }
+  template <bool TINY>
+  __device__ __forceinline__ uint32_t four(float a, float b, float c, float d) const {
+    return __byte_perm(__byte_perm(one<TINY>(a), one<TINY>(b), 0x0040), __byte_perm(one<TINY>(c), one<TINY>(d), 0x0040), 0x5410);
+  }
 };
-__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-}
-
 constexpr int kUnitsPerThread = 4, kHeadsPerThread = 4;
 
 // CTAs below kv_blocks: one page of one sequence, one head, K or V. The new
@@ -279,11 +282,8 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
         load_v<T, 4>(x + int64_t(h) * d + un.c1, q[k]);
       }
     }
-    uint64_t turns[4];
-    if (un.turned) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) turns[e] = a.rope.turns[u * 4 + e];
-    }
+    // the row's cosines once, for all of its heads
+    __shared__ __align__(16) float s_sn[128], s_cs[128];
     int pos = 0;
     if (a.rope.turns && !a.positions) {
       if (!find_place(a.b, row, lane, &pos)) return;
@@ -291,15 +291,21 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
       if (a.rope.turns) pos = a.positions[row];
       if (row < a.b.row_start[0] || row >= a.b.row_start[a.b.n_seqs]) return;
     }
+    if (a.rope.turns) {
+      for (int i = tid; i < a.rope.rot >> 1; i += blockDim.x) {
+        float sn, cs;
+        turn_sincos(a.rope.turns[i] * static_cast<uint64_t>(static_cast<int64_t>(pos)), sn, cs);
+        s_sn[i] = sn * a.rope.factor;
+        s_cs[i] = cs * a.rope.factor;
+      }
+      __syncthreads();
+    }
     if (hl >= head_lanes) return;
     float sn[4], cs[4];
     if (un.turned) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        turn_sincos(turns[e] * static_cast<uint64_t>(static_cast<int64_t>(pos)), sn[e], cs[e]);
-        sn[e] *= a.rope.factor;
-        cs[e] *= a.rope.factor;
-      }
+      const float4 x4 = *reinterpret_cast<const float4*>(s_sn + 4 * u), y4 = *reinterpret_cast<const float4*>(s_cs + 4 * u);
+      sn[0] = x4.x, sn[1] = x4.y, sn[2] = x4.z, sn[3] = x4.w;
+      cs[0] = y4.x, cs[1] = y4.y, cs[2] = y4.z, cs[3] = y4.w;
     }
 #pragma unroll
     for (int k = 0; k < kHeadsPerThread; ++k) {
@@ -384,21 +390,24 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
       uint32_t* cw = &c.x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        uint32_t r[4];
+        float v[4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          r[f] = code(__fmul_rn(static_cast<float>(static_cast<int>((cw[e] >> (8 * f)) & 255u) - 128), old));
-        cw[e] = low_bytes(r[0], r[1], r[2], r[3]);
+        for (int f = 0; f < 4; ++f) v[f] = __fmul_rn(static_cast<float>(static_cast<int>((cw[e] >> (8 * f)) & 255u) - 128), old);
+        cw[e] = code.tiny ? code.four<true>(v[0], v[1], v[2], v[3]) : code.four<false>(v[0], v[1], v[2], v[3]);
       }
       *p = c;
     }
   }
-  each([&](int k, int t, int u) {
-    const Unit un = unit_of<4>(u, turn ? a.rope.rot : 0, il);
-    uint8_t* o = codes + t * d;
-    *reinterpret_cast<uint32_t*>(o + un.c0) = low_bytes(code(va[k][0]), code(va[k][1]), code(va[k][2]), code(va[k][3]));
-    *reinterpret_cast<uint32_t*>(o + un.c1) = low_bytes(code(vb[k][0]), code(vb[k][1]), code(vb[k][2]), code(vb[k][3]));
-  });
+  auto store = [&](auto tiny) {
+    each([&](int k, int t, int u) {
+      const Unit un = unit_of<4>(u, turn ? a.rope.rot : 0, il);
+      uint8_t* o = codes + t * d;
+      *reinterpret_cast<uint32_t*>(o + un.c0) = code.four<decltype(tiny)::value>(va[k][0], va[k][1], va[k][2], va[k][3]);
+      *reinterpret_cast<uint32_t*>(o + un.c1) = code.four<decltype(tiny)::value>(vb[k][0], vb[k][1], vb[k][2], vb[k][3]);
+    });
+  };
+  if (code.tiny) store(std::true_type{});
+  else store(std::false_type{});
   if (tid == 0) *scale_p = scale;
 }
 
