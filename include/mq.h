@@ -456,7 +456,9 @@ MQ_API mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch,
  *   s_j = cap(scale q . k_j),  o = sum_j softmax(s)_j v_j,  lse = ln sum_j e^{s_j}
  * over j <= P (and j > P - window if window > 0), cap(s) = softcap
  * tanh(s / softcap) if softcap > 0. A row that sees no token gets o = 0 and
- * lse = -infinity. What pages hold behind kv_len has no part in it.
+ * lse = -infinity. What pages hold behind kv_len has no part in it, and pages
+ * wholly before every row's window are not looked at (their entries may hold
+ * anything).
  *   q, out : n_rows x n_q_heads x head_dim bf16, rows q_stride / out_stride
  *            elements apart (multiples of 8), 16-byte aligned, not overlapping.
  *   lse    : n_rows x n_q_heads fp32, or NULL.
@@ -473,6 +475,29 @@ MQ_API mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* ba
                                  int64_t q_stride, int64_t n_q_heads, float scale, float softcap,
                                  int64_t window, void* out, int64_t out_stride, float* lse,
                                  void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * The chained decoder stack of mq_chain_forward with attention over each
+ * layer's cache in place of the one-token stand-in. Per layer, behind qkv:
+ * mq_kv_append of its keys and values (rotated if rope is given, at the tokens'
+ * places) into caches[l], then mq_kv_attention of the rotated queries, with
+ * scale 1 / sqrt(head_dim). batch describes the n_rows (1 to 32) rows of h:
+ * one row a sequence is a decode step, several are drafted tokens or a short
+ * prompt; kv_len counts the new tokens. A row of no sequence, or a padded one,
+ * attends to nothing (a = 0).
+ *   caches  : n_layers HOST descriptors, one a layer; each of head_dim and
+ *             Dkv / head_dim heads (head_dim divides D and Dkv).
+ *   scratch : mq_chain_decode_scratch_bytes (device), 256-byte aligned. The
+ *             views of mq_chain_scratch_views hold for it too.
+ * Other arguments and MQ_CHAIN_GRAPH as mq_chain_forward; a replayed graph
+ * reads row_start, kv_len and page_table as they are then.
+ */
+MQ_API size_t mq_chain_decode_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,
+                                            int64_t D, int64_t Dkv, int64_t F);
+MQ_API mq_status mq_chain_decode(const mq_chain_layer* layers, const mq_kv_cache* caches, int n_layers,
+                                 const mq_kv_batch* batch, const mq_rope_positions* rope, float softcap,
+                                 int64_t window, int64_t D, int64_t Dkv, int64_t F, float* h,
+                                 void* scratch, size_t scratch_bytes, int flags, void* stream);
 
 /*
  * The int8 container as a file: the one stored artifact, from which every

@@ -114,6 +114,10 @@ _kv_scratch = _sig("mq_kv_attention_scratch_bytes", ctypes.c_size_t, [_cacheP, _
 _kv_attention = _sig("mq_kv_attention", _int,
                      [_cacheP, _batchP, _vp, _i64, _i64, ctypes.c_float, ctypes.c_float, _i64, _vp,
                       _i64, _vp, _vp, ctypes.c_size_t, _vp])
+_chain_decode_bytes = _sig("mq_chain_decode_scratch_bytes", ctypes.c_size_t, [_cacheP, _batchP, _i64, _i64, _i64])
+_chain_decode = _sig("mq_chain_decode", _int,
+                     [ctypes.POINTER(ChainLayer), _cacheP, _int, _batchP, _ropeP, ctypes.c_float, _i64, _i64, _i64,
+                      _i64, _vp, _vp, ctypes.c_size_t, _int, _vp])
 _c_save = _sig("mq_container_save", _int, [ctypes.c_char_p, _vp, _vp, _vp, _i64, _i64])
 _c_info = _sig("mq_container_info", _int,
                [ctypes.c_char_p, ctypes.POINTER(_i64), ctypes.POINTER(_i64)])
@@ -132,7 +136,8 @@ EXPORTED = ("mq_version", "mq_last_error", "mq_packed_bytes", "mq_quantize_int8"
             "mq_ep_overflow_cols", "mq_linear_ep", "mq_chain_scratch_bytes",
             "mq_chain_forward", "mq_container_save", "mq_container_info", "mq_container_load",
             "mq_chain_scratch_views", "mq_debug_map_table_count", "mq_rope_table", "mq_rope",
-            "mq_kv_append", "mq_kv_read", "mq_kv_attention_scratch_bytes", "mq_kv_attention")
+            "mq_kv_append", "mq_kv_read", "mq_kv_attention_scratch_bytes", "mq_kv_attention",
+            "mq_chain_decode_scratch_bytes", "mq_chain_decode")
 
 NOALLOC_SCRATCH_BYTES = 1280 * 1024
 
@@ -239,9 +244,14 @@ def chain_scratch_views(M: int, D: int, Dkv: int, F: int) -> dict:
 class ChainPlan:
     """Host descriptors of a chained stack, built once and reused. `layers` is
     a list of (r, [qkv, o, gate, up, down]) with each linear a (packed, alpha,
-    zero) triple of device tensors."""
+    zero) triple of device tensors. `caches` (a KVCache a layer) is for decode."""
 
-    def __init__(self, layers, M: int, D: int, Dkv: int, F: int, head_dim: int):
+    def __init__(self, layers, M: int, D: int, Dkv: int, F: int, head_dim: int, caches=None):
+        self.caches = None if caches is None else list(caches)
+        if caches is not None:
+            if len(self.caches) != len(layers):
+                raise ValueError("a cache for each layer")
+            self.cache_arr = (KVCacheDesc * len(layers))(*[c.desc for c in self.caches])
         self.M, self.D, self.Dkv, self.F, self.hd = M, D, Dkv, F, head_dim
         self.n = len(layers)
         self.arr = (ChainLayer * self.n)()
@@ -257,6 +267,25 @@ class ChainPlan:
         nbytes = scratch.numel() * scratch.element_size()
         _check(_chain(self.arr, self.n, self.M, self.D, self.Dkv, self.F, self.hd, _ptr(h),
                       _ptr(scratch), nbytes, MQ_CHAIN_GRAPH if graph else 0, _stream(stream)))
+
+
+    def decode(self, batch, h, scratch, rope=None, softcap: float = 0.0, window: int = 0, graph: bool = False,
+               stream=None) -> None:
+        """One step over the plan's caches: the batch's new tokens, rows of h
+        (n_rows x D fp32) in place. scratch: decode_scratch_bytes."""
+        if self.caches is None:
+            raise ValueError("the plan has no caches")
+        _check(_chain_decode(self.arr, self.cache_arr, self.n, batch.desc, rope.desc if rope is not None else None,
+                             softcap, window, self.D, self.Dkv, self.F, _ptr(h), _ptr(scratch),
+                             scratch.numel() * scratch.element_size(), MQ_CHAIN_GRAPH if graph else 0, _stream(stream)))
+
+    def decode_scratch_bytes(self, batch) -> int:
+        if self.caches is None:
+            raise ValueError("the plan has no caches")
+        n = int(_chain_decode_bytes(self.caches[0].desc, batch.desc, self.D, self.Dkv, self.F))
+        if n == 0:
+            raise MQError(MQ_ERR_INVALID_ARG, last_error())
+        return n
 
 
 class RopeTable:

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdarg>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <map>
@@ -14,6 +15,7 @@
 
 #include "../../include/mq.h"
 #include "mq_device.cuh"
+#include "kv_internal.h"
 #include "mq_internal.h"
 
 namespace mq {
@@ -338,12 +340,8 @@ mq_status mq_chain_scratch_views(int64_t M, int64_t D, int64_t Dkv, int64_t F, m
   return MQ_OK;
 }
 
-mq_status mq_chain_forward(const mq_chain_layer* layers, int n_layers, int64_t M, int64_t D,
-                           int64_t Dkv, int64_t F, int64_t head_dim, float* h, void* scratch,
-                           size_t scratch_bytes, int flags, void* stream) {
-  TraceRange trace_("mq_chain_forward");
-  g_last_error.clear();
-  const char* who = "mq_chain_forward";
+static mq_status check_chain(const char* who, const mq_chain_layer* layers, int n_layers, int64_t M, int64_t D, int64_t Dkv,
+                             int64_t F, int64_t head_dim, const float* h, const void* scratch, int flags) {
   if (!layers || !h || !scratch) return fail(MQ_ERR_INVALID_ARG, "%s: null pointer", who);
   if (n_layers < 1) return fail(MQ_ERR_INVALID_ARG, "%s: n_layers must be >= 1", who);
   if (M < 1 || M > 32) return fail(MQ_ERR_INVALID_ARG, "%s: M must be in [1, 32]", who);
@@ -354,7 +352,10 @@ mq_status mq_chain_forward(const mq_chain_layer* layers, int n_layers, int64_t M
     return fail(MQ_ERR_UNSUPPORTED, "%s: dimensions too large", who);
   if (flags & ~MQ_CHAIN_GRAPH) return fail(MQ_ERR_INVALID_ARG, "%s: unknown flags", who);
   if (!aligned(h, 4) || !aligned(scratch, 256)) return fail(MQ_ERR_INVALID_ARG, "%s: h must be 4-byte and scratch 256-byte aligned", who);
-  if (scratch_bytes < chain_scratch_bytes(M, D, Dkv, F)) return fail(MQ_ERR_INVALID_ARG, "%s: scratch smaller than mq_chain_scratch_bytes", who);
+  return MQ_OK;
+}
+static mq_status check_chain_linears(const char* who, const mq_chain_layer* layers, int n_layers, int64_t M, int64_t D, int64_t Dkv,
+                                     int64_t F, float* h, const void* scratch) {
   const int64_t nout[5] = {D + 2 * Dkv, D, F, F, D};
   const int64_t nin[5] = {D, D, D, D, F};
   for (int l = 0; l < n_layers; ++l) {
@@ -368,9 +369,84 @@ mq_status mq_chain_forward(const mq_chain_layer* layers, int n_layers, int64_t M
       if (st != MQ_OK) return st;
     }
   }
+  return MQ_OK;
+}
+
+mq_status mq_chain_forward(const mq_chain_layer* layers, int n_layers, int64_t M, int64_t D,
+                           int64_t Dkv, int64_t F, int64_t head_dim, float* h, void* scratch,
+                           size_t scratch_bytes, int flags, void* stream) {
+  TraceRange trace_("mq_chain_forward");
+  g_last_error.clear();
+  const char* who = "mq_chain_forward";
+  mq_status st = check_chain(who, layers, n_layers, M, D, Dkv, F, head_dim, h, scratch, flags);
+  if (st != MQ_OK) return st;
+  if (scratch_bytes < chain_scratch_bytes(M, D, Dkv, F)) return fail(MQ_ERR_INVALID_ARG, "%s: scratch smaller than mq_chain_scratch_bytes", who);
+  if ((st = check_chain_linears(who, layers, n_layers, M, D, Dkv, F, h, scratch)) != MQ_OK) return st;
   cudaError_t e = run_chain(layers, n_layers, static_cast<int>(M), static_cast<int>(D), static_cast<int>(Dkv),
                             static_cast<int>(F), static_cast<int>(head_dim), h, scratch,
                             (flags & MQ_CHAIN_GRAPH) != 0, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, who);
+  return MQ_OK;
+}
+
+// Behind the chain's own scratch: the rotated queries, then the attention's scratch.
+static size_t chain_queries_bytes(int64_t M, int64_t D) { return (static_cast<size_t>(M) * D * 2 + 255) & ~size_t(255); }
+
+size_t mq_chain_decode_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch, int64_t D, int64_t Dkv, int64_t F) {
+  g_last_error.clear();
+  if (!cache || !batch || cache->head_dim < 1 || D % cache->head_dim) {
+    fail(MQ_ERR_INVALID_ARG, "mq_chain_decode_scratch_bytes: null or a head_dim that does not divide D");
+    return 0;
+  }
+  const size_t chain = mq_chain_scratch_bytes(batch->n_rows, D, Dkv, F);
+  if (chain == 0) {
+    fail(MQ_ERR_INVALID_ARG, "mq_chain_decode_scratch_bytes: bad sizes");
+    return 0;
+  }
+  const size_t attention = mq_kv_attention_scratch_bytes(cache, batch, D / cache->head_dim);
+  return attention == 0 ? 0 : chain + chain_queries_bytes(batch->n_rows, D) + attention;
+}
+
+mq_status mq_chain_decode(const mq_chain_layer* layers, const mq_kv_cache* caches, int n_layers, const mq_kv_batch* batch,
+                          const mq_rope_positions* rope, float softcap, int64_t window, int64_t D, int64_t Dkv, int64_t F, float* h,
+                          void* scratch, size_t scratch_bytes, int flags, void* stream) {
+  TraceRange trace_("mq_chain_decode");
+  g_last_error.clear();
+  const char* who = "mq_chain_decode";
+  if (!caches || !batch) return fail(MQ_ERR_INVALID_ARG, "%s: null pointer", who);
+  const int64_t M = batch->n_rows, head_dim = caches->head_dim;
+  mq_status st = check_chain(who, layers, n_layers, M, D, Dkv, F, head_dim, h, scratch, flags);
+  if (st != MQ_OK) return st;
+  const size_t chain = chain_scratch_bytes(M, D, Dkv, F), queries = chain_queries_bytes(M, D);
+  if (scratch_bytes < chain + queries) return fail(MQ_ERR_INVALID_ARG, "%s: scratch smaller than mq_chain_decode_scratch_bytes", who);
+  if ((st = check_chain_linears(who, layers, n_layers, M, D, Dkv, F, h, scratch)) != MQ_OK) return st;
+  size_t views[10];
+  chain_views(M, D, Dkv, F, views);
+  uint8_t* base = static_cast<uint8_t*>(scratch);
+  const float* qkv = reinterpret_cast<const float*>(base + views[1]);
+  const int64_t width = D + 2 * Dkv, heads = D / head_dim;
+  ChainCached cached;
+  cached.append.resize(n_layers);
+  cached.attend.resize(n_layers);
+  for (int l = 0; l < n_layers; ++l) {
+    const mq_kv_cache& c = caches[l];
+    char w[64];
+    std::snprintf(w, sizeof(w), "%s[layer %d]", who, l);
+    if (c.head_dim != head_dim || int64_t(c.n_kv_heads) * head_dim != Dkv)
+      return fail(MQ_ERR_INVALID_ARG, "%s: a cache needs head_dim=%lld and Dkv / head_dim heads", w, (long long)head_dim);
+    bool nothing = false;
+    st = kv_append_args(w, &c, batch, qkv + D, qkv + D + Dkv, MQ_F32, width, width, rope, nullptr, qkv, width, heads, base + chain,
+                        &cached.append[l], &nothing);
+    if (st != MQ_OK) return st;
+    if (nothing) return fail(MQ_ERR_INVALID_ARG, "%s: the batch has no rows", w);
+    st = kv_attention_args(w, &c, batch, base + chain, D, heads, static_cast<float>(1.0 / std::sqrt(static_cast<double>(head_dim))),
+                           softcap, window, base + views[2], D, nullptr, base + chain + queries, scratch_bytes - chain - queries,
+                           &cached.attend[l], &nothing);
+    if (st != MQ_OK) return st;
+  }
+  cudaError_t e = run_chain(layers, n_layers, static_cast<int>(M), static_cast<int>(D), static_cast<int>(Dkv), static_cast<int>(F),
+                            static_cast<int>(head_dim), h, scratch, (flags & MQ_CHAIN_GRAPH) != 0,
+                            static_cast<cudaStream_t>(stream), &cached);
   if (e != cudaSuccess) return cuda_fail(e, who);
   return MQ_OK;
 }

@@ -8,7 +8,9 @@
 // paragraph gives each layer its own width). The stand-in glue, per layer:
 //   xn  = bf16(rmsnorm(h))                 RMSNorm, no learned scale, eps 1e-6
 //   qkv = xn . Wqkv^T                      decode GEMV
-//   a   = bf16(v of the head's kv group)   attention over a one-token context
+//   a   = bf16(v of the head's kv group)   attention over a one-token context, or
+//         (mq_chain_decode) qkv's keys and values into the layer's 8-bit cache,
+//         rotated, and attention of the rotated queries over it
 //   h1  = h + a . Wo^T                     decode GEMV, residual
 //   xn1 = bf16(rmsnorm(h1))
 //   g, u = xn1 . Wgate^T, xn1 . Wup^T      one decode launch over both
@@ -19,11 +21,13 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 #include <map>
 #include <mutex>
 #include <vector>
 
 #include "../../include/mq.h"
+#include "kv_internal.h"
 #include "mq_device.cuh"
 #include "mq_internal.h"
 
@@ -155,6 +159,7 @@ struct ChainArgs {
   float* h;
   uint8_t* scratch;
   uint32_t* err;
+  const ChainCached* cached;
 };
 
 // Enqueues the whole chain on `s`.
@@ -172,6 +177,8 @@ cudaError_t enqueue_chain(const ChainArgs& c, const ChainLayout& L, cudaStream_t
   e = launch_pdl(rmsnorm_kernel, dim3(M), dim3(kGlueThreads), 0, s, static_cast<const float*>(c.h), no_add,
                  no_out, bf(L.xn), D, sync);
   if (e != cudaSuccess) return e;
+  // rows of no sequence attend to nothing
+  if (c.cached && (e = cudaMemsetAsync(c.scratch + L.a, 0, size_t(M) * D * 2, s)) != cudaSuccess) return e;
   for (int l = 0; l < c.n_layers; ++l) {
     const mq_chain_layer& Ly = c.layers[l];
     auto job = [&](int which, const void* x, int64_t N, int64_t K, float* y) {
@@ -188,8 +195,16 @@ cudaError_t enqueue_chain(const ChainArgs& c, const ChainLayout& L, cudaStream_t
     };
     LinearJob jq = job(0, bf(L.xn), D + 2 * Dkv, D, fp(L.qkv));
     if ((e = run_gemv_fixed_n(&jq, 1, M, s, fx)) != cudaSuccess) return e;
-    e = launch_pdl(attn_one_token_kernel, dim3(glue_grid(int64_t(M) * D, sms)), dim3(kGlueThreads), 0, s,
-                   static_cast<const float*>(fp(L.qkv)), bf(L.a), M, D, Dkv, c.hd);
+    if (c.cached) {
+      AppendArgs append = c.cached->append[l];
+      AttendArgs attend = c.cached->attend[l];
+      append.err = attend.err = c.err;
+      if ((e = launch_kv_append(append, MQ_F32, s, sms)) != cudaSuccess) return e;
+      e = launch_kv_attention(attend, s, sms);
+    } else {
+      e = launch_pdl(attn_one_token_kernel, dim3(glue_grid(int64_t(M) * D, sms)), dim3(kGlueThreads), 0, s,
+                     static_cast<const float*>(fp(L.qkv)), bf(L.a), M, D, Dkv, c.hd);
+    }
     if (e != cudaSuccess) return e;
     LinearJob jo = job(1, bf(L.a), D, D, fp(L.o));
     if ((e = run_gemv_fixed_n(&jo, 1, M, s, fx)) != cudaSuccess) return e;
@@ -214,6 +229,12 @@ cudaError_t enqueue_chain(const ChainArgs& c, const ChainLayout& L, cudaStream_t
   return cudaSuccess;
 }
 
+uint64_t float_bits(float v) {
+  uint32_t u;
+  std::memcpy(&u, &v, sizeof(u));
+  return u;
+}
+
 // Instantiated graphs of earlier identical calls, keyed by every argument.
 std::mutex g_graph_mutex;
 std::map<std::vector<uint64_t>, cudaGraphExec_t> g_graphs;
@@ -231,12 +252,12 @@ void chain_views(int64_t M, int64_t D, int64_t Dkv, int64_t F, size_t out[10]) {
 }
 
 cudaError_t run_chain(const mq_chain_layer* layers, int n_layers, int M, int D, int Dkv, int F, int hd,
-                      float* h, void* scratch, bool use_graph, cudaStream_t stream) {
+                      float* h, void* scratch, bool use_graph, cudaStream_t stream, const ChainCached* cached) {
   const ChainLayout L = chain_layout(M, D, Dkv, F);
   uint32_t* err = nullptr;
   cudaError_t e = get_error_word(&err);
   if (e != cudaSuccess) return e;
-  const ChainArgs c{layers, n_layers, M, D, Dkv, F, hd, h, static_cast<uint8_t*>(scratch), err};
+  const ChainArgs c{layers, n_layers, M, D, Dkv, F, hd, h, static_cast<uint8_t*>(scratch), err, cached};
   const int sms = sm_count();
   if (!use_graph || stream == nullptr) return enqueue_chain(c, L, stream, sms);
 
@@ -252,6 +273,26 @@ cudaError_t run_chain(const mq_chain_layer* layers, int n_layers, int M, int D, 
       key.push_back(reinterpret_cast<uint64_t>(layers[l].packed[i]));
       key.push_back(reinterpret_cast<uint64_t>(layers[l].alpha[i]));
       key.push_back(reinterpret_cast<uint64_t>(layers[l].zero[i]));
+    }
+  }
+  if (cached) {
+    key.push_back(1);
+    auto batch = [&](const KvBatch& b) {
+      for (const void* p : {static_cast<const void*>(b.row_start), static_cast<const void*>(b.kv_len), static_cast<const void*>(b.pages)})
+        key.push_back(reinterpret_cast<uint64_t>(p));
+      for (int v : {b.n_seqs, b.max_pages, b.n_rows, b.max_new, b.max_len}) key.push_back(uint64_t(v));
+    };
+    batch(cached->append[0].b);
+    const Rope& r = cached->append[0].rope;
+    key.insert(key.end(), {reinterpret_cast<uint64_t>(r.turns), uint64_t(r.rot), uint64_t(r.interleaved), float_bits(r.factor)});
+    const AttendArgs& t = cached->attend[0];
+    key.insert(key.end(), {float_bits(t.scale), float_bits(t.softcap), uint64_t(t.window)});
+    for (const AttendArgs& x : cached->attend) {
+      for (const void* p : {static_cast<const void*>(x.c.k), static_cast<const void*>(x.c.v), static_cast<const void*>(x.c.k_scale),
+                            static_cast<const void*>(x.c.v_scale)})
+        key.push_back(reinterpret_cast<uint64_t>(p));
+      key.push_back(uint64_t(x.c.n_pages));
+      key.push_back(uint64_t(x.c.page));
     }
   }
   std::lock_guard<std::mutex> lk(g_graph_mutex);

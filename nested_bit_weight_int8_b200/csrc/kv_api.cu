@@ -95,7 +95,89 @@ mq_status check_rows(const char* who, const char* what, const void* p, int64_t s
   return MQ_OK;
 }
 
+mq_status check_group(const char* who, const KvCache& c, const KvBatch& b, int64_t n_q_heads, int* group) {
+  if (n_q_heads < c.heads || n_q_heads % c.heads != 0)
+    return refuse(MQ_ERR_INVALID_ARG, "%s: n_q_heads=%lld must be a multiple of n_kv_heads=%d", who, (long long)n_q_heads, c.heads);
+  if (n_q_heads > 16384 || int64_t(b.max_new) * (n_q_heads / c.heads) > (1 << 28))
+    return refuse(MQ_ERR_UNSUPPORTED, "%s: too many query heads or rows", who);
+  *group = static_cast<int>(n_q_heads / c.heads);
+  return MQ_OK;
+}
+
 }  // namespace
+
+mq_status kv_append_args(const char* who, const mq_kv_cache* cache, const mq_kv_batch* batch, const void* k, const void* v, int dtype,
+                         int64_t k_stride, int64_t v_stride, const mq_rope_positions* rope, const int32_t* positions,
+                         const void* q, int64_t q_stride, int64_t n_q_heads, void* q_out, AppendArgs* out, bool* nothing) {
+  AppendArgs& a = *out;
+  a = AppendArgs{};
+  bool empty = false;
+  mq_status st = check_cache(who, cache, &a.c);
+  if (st != MQ_OK) return st;
+  if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
+  if (!is_dtype(dtype)) return refuse(MQ_ERR_INVALID_ARG, "%s: dtype must be MQ_F32 or MQ_BF16", who);
+  const int item = dtype == MQ_F32 ? 4 : 2;
+  const int64_t width = int64_t(a.c.heads) * a.c.d;
+  if ((st = check_rows(who, "k", k, k_stride, width, item, 4)) != MQ_OK) return st;
+  if ((st = check_rows(who, "v", v, v_stride, width, item, 4)) != MQ_OK) return st;
+  if (rope && (st = check_rope(who, rope, a.c.d, 8, &a.rope)) != MQ_OK) return st;
+  if (!on(positions, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", who);
+  if (positions && !rope) return refuse(MQ_ERR_INVALID_ARG, "%s: positions without rope", who);
+  if (q) {
+    if (n_q_heads < 1 || n_q_heads > 65535) return refuse(MQ_ERR_INVALID_ARG, "%s: n_q_heads must be in [1, 65535]", who);
+    if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, item, 4)) != MQ_OK) return st;
+    if (!q_out || !on(q_out, 8)) return refuse(MQ_ERR_INVALID_ARG, "%s: q_out null or not 8-byte aligned", who);
+  } else if (q_out) {
+    return refuse(MQ_ERR_INVALID_ARG, "%s: q_out without q", who);
+  }
+  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
+  if (*nothing) return MQ_OK;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  a.positions = positions;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.n_q_heads = static_cast<int>(n_q_heads);
+  return MQ_OK;
+}
+
+mq_status kv_attention_args(const char* who, const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q, int64_t q_stride,
+                            int64_t n_q_heads, float scale, float softcap, int64_t window, void* out, int64_t out_stride, float* lse,
+                            void* scratch, size_t scratch_bytes, AttendArgs* out_args, bool* nothing) {
+  AttendArgs& a = *out_args;
+  a = AttendArgs{};
+  bool empty = false;
+  mq_status st = check_cache(who, cache, &a.c);
+  if (st != MQ_OK) return st;
+  if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
+  if ((st = check_group(who, a.c, a.b, n_q_heads, &a.group)) != MQ_OK) return st;
+  if (!std::isfinite(scale)) return refuse(MQ_ERR_INVALID_ARG, "%s: scale must be finite", who);
+  if (!std::isfinite(softcap) || softcap < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0 (0: none)", who);
+  if (window < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: window must be >= 0 (0: none)", who);
+  if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
+  if ((st = check_rows(who, "out", out, out_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
+  if (!on(lse, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", who);
+  if (!scratch || !on(scratch, 256)) return refuse(MQ_ERR_INVALID_ARG, "%s: scratch null or not 256-byte aligned", who);
+  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
+  if (*nothing) return MQ_OK;
+  const int sms = sm_count();
+  if (scratch_bytes < kv_attention_scratch(a.c, a.b, a.group, sms))
+    return refuse(MQ_ERR_INVALID_ARG, "%s: scratch smaller than mq_kv_attention_scratch_bytes", who);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.window = window > (1 << 30) ? 0 : static_cast<int>(window);  // longer than any sequence
+  a.out = static_cast<uint16_t*>(out);
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.scratch = static_cast<uint8_t*>(scratch);
+  return MQ_OK;
+}
+
 }  // namespace mq
 
 using namespace mq;
@@ -175,36 +257,11 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
   set_last_error("");
   const char* who = "mq_kv_append";
   AppendArgs a{};
-  bool empty = false;
-  mq_status st = check_cache(who, cache, &a.c);
-  if (st != MQ_OK) return st;
-  if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
-  if (!is_dtype(dtype)) return refuse(MQ_ERR_INVALID_ARG, "%s: dtype must be MQ_F32 or MQ_BF16", who);
-  const int item = dtype == MQ_F32 ? 4 : 2;
-  const int64_t width = int64_t(a.c.heads) * a.c.d;
-  if ((st = check_rows(who, "k", k, k_stride, width, item, 4)) != MQ_OK) return st;
-  if ((st = check_rows(who, "v", v, v_stride, width, item, 4)) != MQ_OK) return st;
-  if (rope && (st = check_rope(who, rope, a.c.d, 8, &a.rope)) != MQ_OK) return st;
-  if (!on(positions, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", who);
-  if (positions && !rope) return refuse(MQ_ERR_INVALID_ARG, "%s: positions without rope", who);
-  if (q) {
-    if (n_q_heads < 1 || n_q_heads > 65535) return refuse(MQ_ERR_INVALID_ARG, "%s: n_q_heads must be in [1, 65535]", who);
-    if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, item, 4)) != MQ_OK) return st;
-    if (!q_out || !on(q_out, 8)) return refuse(MQ_ERR_INVALID_ARG, "%s: q_out null or not 8-byte aligned", who);
-  } else if (q_out) {
-    return refuse(MQ_ERR_INVALID_ARG, "%s: q_out without q", who);
-  }
-  if (empty || a.b.n_rows == 0 || a.b.max_new == 0) return MQ_OK;
-  a.k = k;
-  a.v = v;
-  a.q = q;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.q_stride = q_stride;
-  a.positions = positions;
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.n_q_heads = static_cast<int>(n_q_heads);
-  cudaError_t e = get_error_word(&a.err);
+  bool nothing = false;
+  const mq_status st = kv_append_args(who, cache, batch, k, v, dtype, k_stride, v_stride, rope, positions, q, q_stride, n_q_heads,
+                                      q_out, &a, &nothing);
+  if (st != MQ_OK || nothing) return st;
+  const cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
   return finish(launch_kv_append(a, dtype, static_cast<cudaStream_t>(stream), sm_count()), who);
 }
@@ -242,15 +299,6 @@ mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const i
   return finish(launch_kv_read(a, dtype, static_cast<cudaStream_t>(stream)), who);
 }
 
-static mq_status check_group(const char* who, const KvCache& c, const KvBatch& b, int64_t n_q_heads, int* group) {
-  if (n_q_heads < c.heads || n_q_heads % c.heads != 0)
-    return refuse(MQ_ERR_INVALID_ARG, "%s: n_q_heads=%lld must be a multiple of n_kv_heads=%d", who, (long long)n_q_heads, c.heads);
-  if (n_q_heads > 16384 || int64_t(b.max_new) * (n_q_heads / c.heads) > (1 << 28))
-    return refuse(MQ_ERR_UNSUPPORTED, "%s: too many query heads or rows", who);
-  *group = static_cast<int>(n_q_heads / c.heads);
-  return MQ_OK;
-}
-
 size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch, int64_t n_q_heads) {
   const char* who = "mq_kv_attention_scratch_bytes";
   set_last_error("");
@@ -271,34 +319,13 @@ mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, co
   set_last_error("");
   const char* who = "mq_kv_attention";
   AttendArgs a{};
-  bool empty = false;
-  mq_status st = check_cache(who, cache, &a.c);
-  if (st != MQ_OK) return st;
-  if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
-  if ((st = check_group(who, a.c, a.b, n_q_heads, &a.group)) != MQ_OK) return st;
-  if (!std::isfinite(scale)) return refuse(MQ_ERR_INVALID_ARG, "%s: scale must be finite", who);
-  if (!std::isfinite(softcap) || softcap < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0 (0: none)", who);
-  if (window < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: window must be >= 0 (0: none)", who);
-  if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
-  if ((st = check_rows(who, "out", out, out_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
-  if (!on(lse, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", who);
-  if (!scratch || !on(scratch, 256)) return refuse(MQ_ERR_INVALID_ARG, "%s: scratch null or not 256-byte aligned", who);
-  if (empty || a.b.n_rows == 0 || a.b.max_new == 0) return MQ_OK;
-  const int sms = sm_count();
-  if (scratch_bytes < kv_attention_scratch(a.c, a.b, a.group, sms))
-    return refuse(MQ_ERR_INVALID_ARG, "%s: scratch smaller than mq_kv_attention_scratch_bytes", who);
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_stride;
-  a.scale = scale;
-  a.softcap = softcap;
-  a.window = window > (1 << 30) ? 0 : static_cast<int>(window);  // longer than any sequence
-  a.out = static_cast<uint16_t*>(out);
-  a.out_stride = out_stride;
-  a.lse = lse;
-  a.scratch = static_cast<uint8_t*>(scratch);
-  cudaError_t e = get_error_word(&a.err);
+  bool nothing = false;
+  const mq_status st = kv_attention_args(who, cache, batch, q, q_stride, n_q_heads, scale, softcap, window, out, out_stride, lse,
+                                         scratch, scratch_bytes, &a, &nothing);
+  if (st != MQ_OK || nothing) return st;
+  const cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
-  return finish(launch_kv_attention(a, static_cast<cudaStream_t>(stream), sms), who);
+  return finish(launch_kv_attention(a, static_cast<cudaStream_t>(stream), sm_count()), who);
 }
 
 }  // extern "C"

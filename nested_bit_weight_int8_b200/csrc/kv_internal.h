@@ -6,6 +6,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <vector>
+
+#include "../../include/mq.h"
 
 namespace mq {
 
@@ -98,6 +101,21 @@ struct Scratch;
 size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms);
 cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms);
 cudaError_t launch_kv_attention(const AttendArgs& a, cudaStream_t stream, int sms);
+
+// A chained stack's attention: each layer's launch arguments.
+struct ChainCached {
+  std::vector<AppendArgs> append;
+  std::vector<AttendArgs> attend;
+};
+
+// The checks of mq_kv_append and mq_kv_attention, and their launch arguments but
+// for the error word. *nothing: a well-formed call that has nothing to do.
+mq_status kv_append_args(const char* who, const mq_kv_cache* cache, const mq_kv_batch* batch, const void* k, const void* v, int dtype,
+                         int64_t k_stride, int64_t v_stride, const mq_rope_positions* rope, const int32_t* positions,
+                         const void* q, int64_t q_stride, int64_t n_q_heads, void* q_out, AppendArgs* out, bool* nothing);
+mq_status kv_attention_args(const char* who, const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q, int64_t q_stride,
+                            int64_t n_q_heads, float scale, float softcap, int64_t window, void* out, int64_t out_stride, float* lse,
+                            void* scratch, size_t scratch_bytes, AttendArgs* out_args, bool* nothing);
 
 #ifdef __CUDACC__
 // A sequence of the batch: its first row, its rows and its tokens. A sequence

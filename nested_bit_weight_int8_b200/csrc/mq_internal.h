@@ -161,8 +161,12 @@ size_t chain_scratch_bytes(int64_t M, int64_t D, int64_t Dkv, int64_t F);
 // Offsets of the last layer's intermediates (xn, qkv, a, o, h1, xn1, g, u,
 // act, down) inside the chain's scratch.
 void chain_views(int64_t M, int64_t D, int64_t Dkv, int64_t F, size_t out[10]);
+// `cached` (may be null): attention over each layer's key/value cache in place
+// of the one-token stand-in (mq_chain_decode).
+struct ChainCached;
 cudaError_t run_chain(const struct mq_chain_layer* layers, int n_layers, int M, int D, int Dkv, int F,
-                      int hd, float* h, void* scratch, bool use_graph, cudaStream_t stream);
+                      int hd, float* h, void* scratch, bool use_graph, cudaStream_t stream,
+                      const ChainCached* cached = nullptr);
 void release_chain_graphs();
 // The bounded cache of tensor-map tables of large decode launches: frees all
 // of it (after the devices finish), and its current size.

@@ -228,6 +228,20 @@ def test_two_streams_and_a_graph_that_sees_new_lengths():
     mq.device_status()
 
 
+@pytest.mark.parametrize("n", [1, 3, 200])
+def test_pages_before_the_window_may_be_gone(n):
+    b = Batch([(n, 700), (min(n, 5), 40)], 2, 64, 16, seed=14, fill="all")
+    q = queries(b, 4)
+    window = 100
+    out, log = attend(b, 4, q, window=window)
+    check(b, 4, q, out, log, window=window)
+    gone = (700 - n - window + 1) // 16
+    b.pages[0, :gone] = -1
+    again, log2 = attend(b, 4, q, window=window)
+    mq.device_status()
+    assert torch.equal(out, again) and torch.equal(log, log2)
+
+
 def test_bad_pages_and_bounds_are_reported():
     for spoil in ("page", "length", "rows"):
         b = Batch([(1, 40), (1, 33)], 1, 64, 16, seed=12, max_len=40, fill="all")

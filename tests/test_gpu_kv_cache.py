@@ -226,3 +226,42 @@ def test_batches_that_do_not_keep_their_bounds_are_reported_and_touch_nothing():
         p = b.table[0, :2]
         assert np.array_equal(codes[p], b.codes[0][p]), spoil
         mq.device_status()  # read and cleared
+
+
+@pytest.mark.parametrize("low,high", [(-38, -30), (-44, -37), (-31, -29), (-3, 3), (20, 36)])
+def test_codes_of_tiny_and_huge_values(low, high):
+    # every quotient as correctly rounded, from subnormal scales to the largest
+    b = Batch([(33, 70), (5, 5), (1, 16)], 2, 64, 16, seed=5)
+    rng = np.random.default_rng(low + 100)
+    with np.errstate(all="ignore"):
+        x = (rng.standard_normal((b.rows, 2, 64)) * 10.0 ** rng.uniform(low, high, (b.rows, 2, 1))).astype(np.float32)
+    x[3] = 0
+    b.scales[0][:] = b.scales[1][:] = np.float32(10.0 ** low)
+    b.ks.copy_(torch.from_numpy(b.scales[0]))
+    b.vs.copy_(torch.from_numpy(b.scales[1]))
+    rows = torch.from_numpy(x).to(DEV).view(b.rows, -1)
+    mq.kv_append(b.cache, b.batch, rows, rows, mq.MQ_F32, 128, 128)
+    mq.device_status()
+    for which in range(2):
+        codes, scales = expect(b, which, x)
+        got_c, got_s = b.host(which)
+        assert np.array_equal(got_s, scales) and np.array_equal(got_c, codes)
+
+
+def test_more_sequences_than_one_round_finds():
+    # the queries' search for their sequence beyond 32 sequences, and empty ones among them
+    lengths = [(int(n), int(n) + int(c)) for n, c in np.random.default_rng(1).integers(0, 4, (150, 2))]
+    b = Batch(lengths, 1, 64, 16, seed=6, tail_rows=3)
+    table = mq.RopeTable(10000.0, 64, device=DEV)
+    qkv = torch.randn(b.rows, 4 * 64, device=DEV)
+    q = torch.full((b.rows, 2 * 64), 9.0, device=DEV, dtype=torch.bfloat16)
+    mq.kv_append(b.cache, b.batch, qkv[:, 128:], qkv[:, 192:], mq.MQ_F32, 256, 256, rope=table, q=qkv, q_stride=256, n_q_heads=2,
+                 q_out=q)
+    mq.device_status()
+    places = np.concatenate([b.places(s) for s in range(len(lengths))])
+    w, f = orope.frequencies(10000.0, 64)
+    x = qkv.cpu().numpy().astype(np.float64)[:len(places), :128].reshape(-1, 2, 64)
+    want, tol = orope.rotate(x, places, w, f, "half"), orope.f32_error(x, 64, f, "half")
+    got = q.float().cpu().numpy()
+    assert np.all(np.abs(got[:len(places)].reshape(-1, 2, 64) - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-30)
+    assert np.all(got[len(places):] == 9.0)

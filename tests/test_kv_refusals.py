@@ -149,3 +149,40 @@ def test_the_python_descriptors_refuse_other_layouts():
             mq.KVBatch(*bad, 2, 1, 8)
     with pytest.raises(ValueError):
         mq.RopeTable(1e4, 64, scaling="yarn", params=(2.0,))
+
+
+def chain_layer():
+    layer = mq.ChainLayer()
+    layer.r = 4
+    for i in range(5):
+        layer.packed[i] = layer.alpha[i] = layer.zero[i] = F
+    return layer
+
+
+CHAIN = dict(layers=(mq.ChainLayer * 1)(chain_layer()), caches=cache(), n=1, b=batch(), rope=rope(), cap=0.0, window=0, D=512, Dkv=256,
+             F=1024, h=F, scr=F, size=1 << 40, flags=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(layers=None), BAD), (dict(caches=None), BAD), (dict(b=None), BAD), (dict(n=0), BAD), (dict(h=None), BAD), (dict(h=F + 2), BAD),
+    (dict(scr=F + 128), BAD), (dict(size=64), BAD), (dict(flags=2), BAD), (dict(D=500), BAD), (dict(Dkv=128), BAD),
+    (dict(Dkv=200), BAD), (dict(b=batch(n_rows=0)), BAD), (dict(b=batch(n_rows=33)), BAD), (dict(b=batch(n_seqs=0)), BAD),
+    (dict(b=batch(max_new=0)), BAD), (dict(b=batch(max_len=257)), BAD), (dict(caches=cache(head_dim=24)), BAD),
+    (dict(caches=cache(n_kv_heads=1)), BAD), (dict(caches=cache(k=None)), BAD), (dict(rope=rope(rot_dim=20)), NOT_SERVED),
+    (dict(cap=-1.0), BAD), (dict(window=-1), BAD)])
+def test_chain_decode_refuses(kw, want):
+    assert call(mq._chain_decode, CHAIN, **kw) == want, kw
+    assert "mq_chain_decode" in mq.last_error()
+
+
+def test_chain_decode_scratch_bytes():
+    small = mq._chain_decode_bytes(cache(), batch(), 512, 256, 1024)
+    assert small > mq.chain_scratch_bytes(2, 512, 256, 1024) and small % 256 == 0
+    assert mq._chain_decode_bytes(cache(), batch(n_rows=33), 512, 256, 1024) == 0
+    assert mq._chain_decode_bytes(cache(), batch(), 500, 256, 1024) == 0
+    assert mq._chain_decode_bytes(None, batch(), 512, 256, 1024) == 0
+    plan = mq.ChainPlan([], 1, 512, 256, 1024, 128)
+    with pytest.raises(ValueError):
+        plan.decode_scratch_bytes(None)
+    with pytest.raises(ValueError):
+        mq.ChainPlan([], 1, 512, 256, 1024, 128, caches=[None])
