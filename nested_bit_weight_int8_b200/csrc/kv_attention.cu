@@ -243,7 +243,6 @@ struct Worker {
     // -128 2^-24 times the query's own sum.
     uint32_t qf[NR][kJ * 4][2];
     float fac[NR][2], bias[NR][2];   // of rows 2 t, 2 t + 1
-    int place[NR][2];
     const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -265,7 +264,6 @@ struct Worker {
       ex = ex < 1 || ex > 253 ? 127 : ex;
       const float down = __int_as_float((254 - ex) << 23) * sign;
       const float up = __int_as_float(ex << 23) * fabsf(a.scale) * (a.softcap > 0.f ? 1.f : kLog2e);
-      const int pl = lr < it.rows ? sq.len - sq.n + (first_row + lr) / a.group : -1;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
@@ -287,7 +285,6 @@ struct Worker {
       for (int e = 0; e < 2; ++e) {
         fac[r][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
         bias[r][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e)) * (-128.f * kCode);
-        place[r][e] = __shfl_sync(0xffffffffu, pl, 4 * (2 * t + e));
       }
     }
 
@@ -306,7 +303,7 @@ struct Worker {
     // the places of the tile's first and last query token
     const int lo_place = sq.len - sq.n + it.i0;
     const int hi_place = sq.len - sq.n + (first_row + it.rows - 1) / a.group;
-    const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     // where this lane's chunks lie in a box: K rows g ^ ((g & 1) << 2) and + 8, V rows 2 t, (2 t + 1) ^ 4 and + 8
     const int krow = g ^ ((g & 1) << 2), va_row = 2 * t, vb_row = (2 * t + 1) ^ 4;
 
@@ -372,18 +369,39 @@ struct Worker {
         for (int gi = 0; gi < S::kGroups; ++gi)
 #pragma unroll
           for (int e = 0; e < 2; ++e) f[r][gi][e] *= 1.f / kCode;
-      if (masked || a.softcap > 0.f) {
+      if (a.softcap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int gi = 0; gi < S::kGroups; ++gi) {
+            const float k[2] = {f[r][gi][0] * cap_in, f[r][gi][1] * cap_in};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = sc[r][gi][e] * f[r][gi][e & 1];
-              if (a.softcap > 0.f) x = cap_out * tanh_fast(x * cap_in);
-              const int j = jt + gi * 16 + krow + 8 * (e >> 1), p = place[r][e & 1];
-              if (j > p || (a.window > 0 && j <= p - a.window) || vs[gi] < 0.f) x = -INFINITY;
-              sc[r][gi][e] = x;
+              float y;
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp2_fast(sc[r][gi][e] * k[e & 1])));
+              sc[r][gi][e] = fmaf(-2.f * cap_out, y, cap_out);
+            }
+            f[r][gi][0] = f[r][gi][1] = 1.f;
+          }
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          // places of rows 2 t, 2 t + 1: found again where they matter, for the registers' sake
+          int place[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int lr = 8 * r + 2 * t + e;
+            place[e] = lr < it.rows ? sq.len - sq.n + (first_row + lr) / a.group : -1;
+          }
+#pragma unroll
+          for (int gi = 0; gi < S::kGroups; ++gi) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = jt + gi * 16 + krow + 8 * (e >> 1), p = place[e & 1];
+              const bool off = j > p || (a.window > 0 && j <= p - a.window) || vs[gi] < 0.f;
+              sc[r][gi][e] = off ? -INFINITY : sc[r][gi][e] * f[r][gi][e & 1];
             }
             f[r][gi][0] = f[r][gi][1] = 1.f;
           }
