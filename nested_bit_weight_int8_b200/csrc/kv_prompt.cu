@@ -594,6 +594,10 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       if (!ok) break;
       if (m != -INFINITY) l += sum;
       tc05::wait_st();
+      // A wait on a barrier tells a phase from the one before it only, so no warp may leave a
+      // tile's products further behind. Two tiles of rows: the scores came after them. S twice
+      // in turn: they may still run, and this tile's cannot start before this warp arrives.
+      if (P::kMt == 1 && i > w.t0 && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
       tc05::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.p_full[slot]);
@@ -602,9 +606,6 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     if (!ok) break;
     // ---- outputs, or this piece's sums
     const bool any = w.t0 < w.t1;
-    // A warp may be done with a piece's last tile while the products of the one before
-    // still run (S twice in turn): that phase first, a barrier's wait tells only two apart.
-    if (P::kMt == 1 && w.t1 - w.t0 > 1 && !(ok = wait(&bar.o_done[mt], tick & 1, kErrMma))) break;
     if (any && !(ok = wait(&bar.o_done[mt], (tick - 1) & 1, kErrMma))) break;
     tc05::fence_after_sync();
     // (through the queries' shared memory, which no product reads any more)

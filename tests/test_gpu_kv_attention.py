@@ -183,9 +183,11 @@ def test_the_same_call_gives_the_same_bits_and_strides_do_not_matter():
         assert torch.equal(o, outs[0][0]) and (l is None or torch.equal(l, outs[0][1]))
 
 
-@pytest.mark.parametrize("heads,group,dim,page", [(1, 1, 64, 16), (2, 4, 128, 64), (1, 1, 192, 64), (1, 2, 256, 32)])
-def test_prompts_give_the_same_bits_every_time(heads, group, dim, page):
-    seqs = [(300, 300), (1, 500), (129, 700), (65, 65), (257, 900)]
+@pytest.mark.parametrize("heads,group,dim,page,seqs", [
+    (1, 1, 64, 16, None), (2, 4, 128, 64, None), (1, 1, 192, 64, None), (1, 2, 256, 32, None),
+    (4, 8, 256, 64, [(9, 500 + 37 * i) for i in range(16)]), (4, 8, 128, 64, [(17, 300 + 91 * i) for i in range(16)])])
+def test_prompts_give_the_same_bits_every_time(heads, group, dim, page, seqs):
+    seqs = seqs or [(300, 300), (1, 500), (129, 700), (65, 65), (257, 900)]
     b = Batch(seqs, heads, dim, page, seed=11, fill="all")
     q = queries(b, heads * group)
     out, log = attend(b, heads * group, q)
