@@ -282,7 +282,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   // This kernel follows kv_attend_kernel, which starts its dependents only when what came
   // before it is complete: so this one may begin at once, beside it, and waits for it at its
   // end, for the next kernel's sake.
-  // ---- units before each run of sequences: a warp sums a run
+  // ---- units before each run of sequences
   const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
   auto seq_units = [&](int s) {  // of one sequence, by the warp
     const Seq sq = load_seq(a.b, s, nullptr);
@@ -293,12 +293,22 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
     return units * a.c.heads;
   };
-  s_pre[tid + 1] = 0;
-  __syncthreads();
-  for (int run = warp; run * per < a.b.n_seqs; run += kWarps) {
+  {  // a thread a run, neighbouring runs in different warps; sequences of many items by the warp
+    const int run = lane * kWarps + warp;
     int64_t units = 0;
-    for (int s = run * per; s < min((run + 1) * per, a.b.n_seqs); ++s) units += seq_units(s);
-    if (lane == 0) s_pre[run + 1] = units;
+    for (int k = 0; k < per; ++k) {
+      const int s = run * per + k;
+      const Seq sq = s < a.b.n_seqs ? load_seq(a.b, s, nullptr) : Seq{0, 0, 0};
+      const int nrt = item_rows<D>(a, sq, limit);
+      if (nrt <= 4)
+        for (int rt = 0; rt < nrt; ++rt) units += int64_t(item_of<D>(a, sq, rt).units) * a.c.heads;
+      for (unsigned many = __ballot_sync(0xffffffffu, nrt > 4); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const int64_t u = seq_units(__shfl_sync(0xffffffffu, s, src));
+        if (lane == src) units += u;
+      }
+    }
+    s_pre[run + 1] = units;
   }
   __syncthreads();
   int64_t inc = s_pre[tid + 1];
