@@ -415,7 +415,9 @@ kv_append_kernel(const AppendArgs a, int page_slots, int kv_blocks, int q_splits
 constexpr int kReadThreads = 128;
 
 // One CTA per (page of a sequence's range, head, K or V): bytes in, values
-// out, 16 bytes of output a thread and step.
+// out, 16 bytes of output a thread and step, four steps' loads on their way. Bound
+// by the bytes; conversions through the exponent of 2^23 and a walk without divisions
+// keep the instructions below them.
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads)
 kv_read_kernel(const ReadArgs a) {
@@ -444,26 +446,42 @@ kv_read_kernel(const ReadArgs a) {
   const float scale = (is_v ? a.c.v_scale : a.c.k_scale)[tile];
   const uint8_t* codes = (is_v ? a.c.v : a.c.k) + tile * a.c.page * d;
   T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + (int64_t(o0) + base - first) * a.out_stride + int64_t(h) * d;
-  const int per_row = d / V;
-  for (int w = lo * per_row + threadIdx.x; w < hi * per_row; w += kReadThreads) {
-    const int t = w / per_row, c = (w - t * per_row) * V;
-    float v[V];
-    uint32_t u[V / 4];
-    if constexpr (V == 8) {
-      const uint2 g = *reinterpret_cast<const uint2*>(codes + t * d + c);
-      u[0] = g.x;
-      u[1] = g.y;
-    } else {
-      u[0] = *reinterpret_cast<const uint32_t*>(codes + t * d + c);
+  const int per_row = d / V, step_t = kReadThreads / per_row, step_c = kReadThreads - step_t * per_row;
+  int t = lo + threadIdx.x / per_row, c = threadIdx.x % per_row;
+  constexpr int kSteps = 4;
+  while (t < hi) {
+    uint32_t u[kSteps][V / 4];
+    int at[kSteps], col[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      at[k] = t;
+      col[k] = c * V;
+      if (t < hi) {
+        if constexpr (V == 8) {
+          const uint2 g = *reinterpret_cast<const uint2*>(codes + t * d + c * V);
+          u[k][0] = g.x;
+          u[k][1] = g.y;
+        } else {
+          u[k][0] = *reinterpret_cast<const uint32_t*>(codes + t * d + c * V);
+        }
+      }
+      t += step_t;
+      c += step_c;
+      if (c >= per_row) c -= per_row, ++t;
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      v[e] = __fmul_rn(scale, static_cast<float>(static_cast<int>((u[e / 4] >> (8 * (e % 4))) & 255u) - 128));
-    T* o = out + t * a.out_stride + c;
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    for (int k = 0; k < kSteps; ++k) {
+      if (at[k] >= hi) break;
+      float v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e)  // 2^23 + byte, less 2^23 + 128: exact
+        v[e] = __fmul_rn(scale, __uint_as_float(__byte_perm(u[k][e / 4], 0x4B000000u, 0x7440 + e % 4)) - 8388736.f);
+      T* o = out + at[k] * a.out_stride + col[k];
+      if constexpr (V == 8) {
+        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      } else {
+        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
   }
 }
