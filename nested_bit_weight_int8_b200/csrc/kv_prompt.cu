@@ -111,19 +111,19 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// D: the head's size rounded up to 64, 128 or 256.
-template <int D>
+// D: the head's size rounded up to 64, 128 or 256. MT: tiles of 128 rows, 2 where one's
+// softmax can run beside the other's products, 1 with S twice in turn where there is one (no
+// sequence of the call has more rows) or room for one (at D = 256 the outputs take half of
+// the tensor memory).
+template <int D, int MT>
 struct Plan {
-  // At D = 256 the outputs take half of the tensor memory: one tile of rows, S
-  // twice in turn. Else two tiles of rows, so that one's softmax runs beside the
-  // other's products.
-  static constexpr int kMt = D == 256 ? 1 : 2;
+  static constexpr int kMt = MT;
   static constexpr int kT = D == 256 ? 64 : 128;
   static constexpr int kSoft = 4 * kMt;
-  static constexpr int kConv = D == 256 ? 8 : 4;
+  static constexpr int kConv = MT == 1 ? 8 : 4;
   static constexpr int kThreads = 512;  // the last four warps: one issues the products
   // Registers of a softmax, a spreading and a product thread; the launch gives 128.
-  static constexpr int kSoftRegs = D == 256 ? 208 : 168, kConvRegs = 112, kMmaRegs = 64;
+  static constexpr int kSoftRegs = MT == 1 ? 208 : 168, kConvRegs = 112, kMmaRegs = 64;
   static_assert(kSoft * kSoftRegs + kConv * kConvRegs + 4 * kMmaRegs <= kThreads / 32 * 128, "the split fits the launch's registers");
   static constexpr int kRows = 128 * kMt;
   static constexpr int kGroups = kT / 16;
@@ -163,9 +163,9 @@ struct Item {
   int n;            // tiles; 0 where no row sees a token
   int start, units; // in the split: before the first tile, and in all
 };
-template <int D>
+template <int D, int MT>
 __device__ __forceinline__ Item item_of(const AttendArgs& a, const Seq& sq, int rt) {
-  using P = Plan<D>;
+  using P = Plan<D, MT>;
   Item t;
   const int all = sq.n * a.group;
   t.row0 = rt * P::kRows;
@@ -180,10 +180,10 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, const Seq& sq, int 
   t.units = t.n > 0 ? t.n + P::kStart : 1;
   return t;
 }
-template <int D>
+template <int D, int MT>
 __device__ __forceinline__ int item_rows(const AttendArgs& a, const Seq& sq, int limit) {
   const int all = sq.n * a.group;
-  return all <= limit ? 0 : (all + Plan<D>::kRows - 1) / Plan<D>::kRows;
+  return all <= limit ? 0 : (all + Plan<D, MT>::kRows - 1) / Plan<D, MT>::kRows;
 }
 
 // A piece of an item, as the CTA's warps take it from shared memory.
@@ -200,7 +200,7 @@ struct Piece {
 struct Place {
   int s, rt, h, u0;
 };
-template <int D>
+template <int D, int MT>
 struct Walk {
   Place at;
   Seq sq;
@@ -218,7 +218,7 @@ struct Walk {
     at = p;
     left = units;
     sq = load_seq(a.b, at.s, nullptr);
-    it = item_of<D>(a, sq, at.rt);
+    it = item_of<D, MT>(a, sq, at.rt);
     piece();
   }
   __device__ __forceinline__ bool next(const AttendArgs& a, int limit) {
@@ -230,20 +230,20 @@ struct Walk {
       if (--at.rt < 0) {
         do {
           sq = load_seq(a.b, ++at.s, nullptr);
-          at.rt = item_rows<D>(a, sq, limit) - 1;
+          at.rt = item_rows<D, MT>(a, sq, limit) - 1;
         } while (at.rt < 0);
       }
-      it = item_of<D>(a, sq, at.rt);
+      it = item_of<D, MT>(a, sq, at.rt);
     }
     piece();
     return true;
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(Plan<D>::kThreads, 1)
+template <int D, int MT>
+__global__ void __launch_bounds__(Plan<D, MT>::kThreads, 1)
 kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait_ns) {
-  using P = Plan<D>;
+  using P = Plan<D, MT>;
   constexpr int kT = P::kT, kThreads = P::kThreads, kWarps = kThreads / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bar;
@@ -286,9 +286,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
   const int per = (a.b.n_seqs + kThreads - 1) / kThreads;
   auto seq_units = [&](int s) {  // of one sequence, by the warp
     const Seq sq = load_seq(a.b, s, nullptr);
-    const int nrt = item_rows<D>(a, sq, limit);
+    const int nrt = item_rows<D, MT>(a, sq, limit);
     int64_t units = 0;
-    for (int rt = lane; rt < nrt; rt += 32) units += item_of<D>(a, sq, rt).units;
+    for (int rt = lane; rt < nrt; rt += 32) units += item_of<D, MT>(a, sq, rt).units;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
     return units * a.c.heads;
@@ -299,9 +299,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     for (int k = 0; k < per; ++k) {
       const int s = run * per + k;
       const Seq sq = s < a.b.n_seqs ? load_seq(a.b, s, nullptr) : Seq{0, 0, 0};
-      const int nrt = item_rows<D>(a, sq, limit);
+      const int nrt = item_rows<D, MT>(a, sq, limit);
       if (nrt <= 4)
-        for (int rt = 0; rt < nrt; ++rt) units += int64_t(item_of<D>(a, sq, rt).units) * a.c.heads;
+        for (int rt = 0; rt < nrt; ++rt) units += int64_t(item_of<D, MT>(a, sq, rt).units) * a.c.heads;
       for (unsigned many = __ballot_sync(0xffffffffu, nrt > 4); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const int64_t u = seq_units(__shfl_sync(0xffffffffu, s, src));
@@ -889,9 +889,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       ++s;
     }
     const Seq sq = load_seq(a.b, s, nullptr);
-    for (int first = item_rows<D>(a, sq, limit) - 1;; first -= 32) {
+    for (int first = item_rows<D, MT>(a, sq, limit) - 1;; first -= 32) {
       const int rt = first - lane;
-      const int units = rt >= 0 ? item_of<D>(a, sq, rt).units : 0;
+      const int units = rt >= 0 ? item_of<D, MT>(a, sq, rt).units : 0;
       int64_t upto = int64_t(units) * a.c.heads;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -913,7 +913,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       }
       off -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    Walk<D> w;
+    Walk<D, MT> w;
     w.start(a, at, B - A);
     int k = 0;
     auto publish = [&](int n) {
@@ -963,36 +963,42 @@ kv_prompt_join_kernel(const AttendArgs a, const Scratch sc, const Scratch few) {
   }
 }
 
-template <int D>
+template <int D, int MT>
 size_t layout(const KvCache& c, const KvBatch& b, int group, int sms, Scratch* sc = nullptr, uint8_t* base = nullptr) {
-  const int rows = part_rows(b.max_new, group, Plan<D>::kRows), floats = part_floats(rows, c.d);
+  const int rows = part_rows(b.max_new, group, Plan<D, MT>::kRows), floats = part_floats(rows, c.d);
   const size_t open = align256(size_t(sms) * sizeof(Open));
   if (sc) *sc = Scratch{nullptr, reinterpret_cast<float*>(base + open), reinterpret_cast<Open*>(base), rows, floats};
   return open + align256(size_t(2) * sms * floats * 4);
 }
 
-template <int D>
+template <int D, int MT>
 cudaError_t launch(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms) {
-  using P = Plan<D>;
-  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+  using P = Plan<D, MT>;
+  cudaError_t e = cudaFuncSetAttribute(kv_prompt_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
   if (e != cudaSuccess) return e;
   Scratch sc;
-  layout<D>(a.c, a.b, a.group, sms, &sc, scratch);
-  e = launch_pdl(kv_prompt_kernel<D>, dim3(sms), dim3(P::kThreads), P::kSmem, stream, a, sc, limit, wait_limit_ns());
+  layout<D, MT>(a.c, a.b, a.group, sms, &sc, scratch);
+  e = launch_pdl(kv_prompt_kernel<D, MT>, dim3(sms), dim3(P::kThreads), P::kSmem, stream, a, sc, limit, wait_limit_ns());
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_prompt_join_kernel<D>, dim3(sms, kJoinShare + few.rows), dim3(kJoinWarps * 32), 0, stream, a, sc, few);
 }
 
 }  // namespace
 
+// One tile of rows does for calls whose sequences have up to 128 rows.
+static bool one_tile(int64_t max_new, int group) { return max_new * group <= 128; }
+
 size_t kv_prompt_scratch(const KvCache& c, const KvBatch& b, int group, int sms) {
-  return c.d <= 64 ? layout<64>(c, b, group, sms) : c.d <= 128 ? layout<128>(c, b, group, sms) : layout<256>(c, b, group, sms);
+  if (c.d > 128) return layout<256, 1>(c, b, group, sms);
+  if (one_tile(b.max_new, group)) return c.d <= 64 ? layout<64, 1>(c, b, group, sms) : layout<128, 1>(c, b, group, sms);
+  return c.d <= 64 ? layout<64, 2>(c, b, group, sms) : layout<128, 2>(c, b, group, sms);
 }
 
 cudaError_t launch_kv_prompt(const AttendArgs& a, int limit, const Scratch& few, uint8_t* scratch, cudaStream_t stream, int sms) {
-  if (a.c.d <= 64) return launch<64>(a, limit, few, scratch, stream, sms);
-  if (a.c.d <= 128) return launch<128>(a, limit, few, scratch, stream, sms);
-  return launch<256>(a, limit, few, scratch, stream, sms);
+  if (a.c.d > 128) return launch<256, 1>(a, limit, few, scratch, stream, sms);
+  if (one_tile(a.b.max_new, a.group))
+    return a.c.d <= 64 ? launch<64, 1>(a, limit, few, scratch, stream, sms) : launch<128, 1>(a, limit, few, scratch, stream, sms);
+  return a.c.d <= 64 ? launch<64, 2>(a, limit, few, scratch, stream, sms) : launch<128, 2>(a, limit, few, scratch, stream, sms);
 }
 
 }  // namespace mq

@@ -98,6 +98,111 @@ def test_prompts_beside_single_tokens(heads, group, dim, page, window, softcap):
     check(b, heads * group, q, out, log, softcap, window)
 
 
+@pytest.mark.parametrize("heads,group,dim,page", [(1, 3, 80, 16), (2, 1, 16, 32), (1, 2, 144, 64), (1, 1, 240, 16), (1, 40, 128, 32),
+                                                  (1, 40, 256, 64), (2, 5, 48, 128)])
+def test_prompts_of_odd_heads_and_wide_groups(heads, group, dim, page):
+    seqs = [(150, 210), (1, 90), (3, 3), (33, 500), (1, 0)]
+    b = Batch(seqs, heads, dim, page, seed=21, tail_rows=3, fill="all")
+    q = queries(b, heads * group)
+    out, log = attend(b, heads * group, q)
+    mq.device_status()
+    check(b, heads * group, q, out, log)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompts_with_padded_rows_and_rows_that_see_nothing(dim):
+    # more rows than tokens: the first rows stand before the sequence and see nothing
+    seqs = [(300, 0), (257, 100), (129, 129), (200, 1), (1, 0), (2, 900), (260, 0)]
+    b = Batch(seqs, 2, dim, 32, seed=22, tail_rows=1, fill="all")
+    for window in (0, 7):
+        q = queries(b, 4)
+        out, log = attend(b, 4, q, window=window)
+        mq.device_status()
+        check(b, 4, q, out, log, window=window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompts_whose_scores_rise_and_scales_differ(dim):
+    # each page's keys score higher than all before, V's scales jump over many
+    # orders: the running maximum and the largest scale rise again and again
+    b = Batch([(270, 900), (130, 513)], 1, dim, 16, seed=23, fill="all")
+    rng = np.random.default_rng(23)
+    for s in range(2):
+        for j, page in enumerate(b.table[s]):
+            if page >= 0:
+                b.scales[0][page] = 0.002 * 1.12 ** j
+                b.scales[1][page] = 10.0 ** rng.uniform(-20, 3)
+    b.ks.copy_(torch.from_numpy(b.scales[0]))
+    b.vs.copy_(torch.from_numpy(b.scales[1]))
+    for size in (0.0, 0.3, 3.0):
+        q = queries(b, 2, seed=int(size * 10), size=size)
+        out, log = attend(b, 2, q)
+        mq.device_status()
+        check(b, 2, q, out, log)
+    b.scales[0][:] = b.scales[1][:] = 0
+    b.ks.zero_()
+    b.vs.zero_()
+    out, log = attend(b, 2, q)
+    check(b, 2, q, out, log)
+
+
+@pytest.mark.parametrize("seqs", [[(3, 200), (1, 17)], [(200, 300), (1, 17)]])
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_of_either_sign(seqs, scale):
+    b = Batch(seqs, 1, 128, 32, seed=24, fill="all")
+    q = queries(b, 4)
+    for cap in (0.0, 5.0):
+        out, log = attend(b, 4, q, softcap=cap, scale=scale)
+        mq.device_status()
+        check(b, 4, q, out, log, softcap=cap, scale=scale)
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_nan_and_infinite_queries_stay_in_their_rows_of_a_prompt(dim):
+    b = Batch([(300, 350), (1, 9)], 1, dim, 16, seed=25, fill="all")
+    q = queries(b, 1)
+    bad = torch.zeros(b.rows, dtype=torch.bool, device=DEV)
+    for row, value in ((5, "nan"), (131, "inf"), (299, "-inf")):
+        q[row, row % dim] = float(value)
+        bad[row] = True
+    out, log = attend(b, 1, q)
+    mq.device_status()
+    # (not bit by bit: rows of a warp raise their maxima together)
+    check(b, 1, q, out, log, rows=[r for r in range(300) if not bad[r]])
+    assert torch.all(~torch.isfinite(out[bad])) and torch.all(~torch.isfinite(log[bad]))
+
+
+def test_two_prompt_calls_at_once_and_a_graph_that_sees_new_lengths():
+    for dim in (64, 128, 256):
+        b = Batch([(260, 700), (1, 90), (140, 300)], 2, dim, 64, seed=26, fill="all")
+        q = queries(b, 8)
+        want = {}
+        for c in (700, 650, 100):
+            b.kv_len[0] = c
+            want[c] = [t.clone() for t in attend(b, 8, q)]
+        b.kv_len[0] = 700
+        size = mq.kv_attention_scratch_bytes(b.cache, b.batch, 8)
+        scr = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, m in zip(streams, scr):
+                with torch.cuda.stream(s):
+                    got.append(attend(b, 8, q, stream=s, scratch=m))
+        torch.cuda.synchronize()
+        for o, l in got:
+            assert torch.equal(o, want[700][0]) and torch.equal(l, want[700][1])
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            out, log = attend(b, 8, q, stream=torch.cuda.current_stream(), scratch=scr[0])
+        for c in (650, 100, 700):
+            b.kv_len[0] = c
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[c][0]) and torch.equal(log, want[c][1])
+        mq.device_status()
+
+
 def test_a_long_cache_and_many_sequences():
     b = Batch([(1, 70001)], 2, 128, 128, seed=1, fill="all")
     q = queries(b, 8)
@@ -244,9 +349,10 @@ def test_pages_before_the_window_may_be_gone(n):
     assert torch.equal(out, again) and torch.equal(log, log2)
 
 
-def test_bad_pages_and_bounds_are_reported():
+@pytest.mark.parametrize("n", [1, 200])
+def test_bad_pages_and_bounds_are_reported(n):
     for spoil in ("page", "length", "rows"):
-        b = Batch([(1, 40), (1, 33)], 1, 64, 16, seed=12, max_len=40, fill="all")
+        b = Batch([(1, 40), (n, 33)], 1, 64, 16, seed=12, max_len=40, fill="all")
         q = queries(b, 2)
         out, _ = attend(b, 2, q)
         mq.device_status()
@@ -255,7 +361,7 @@ def test_bad_pages_and_bounds_are_reported():
         elif spoil == "length":
             b.kv_len[1] = 41
         else:
-            b.row_start[2] = 3
+            b.row_start[2] = n + 2
         again, _ = attend(b, 2, q)
         with pytest.raises(mq.MQError) as e:
             mq.device_status()
