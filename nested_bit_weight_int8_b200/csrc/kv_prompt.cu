@@ -429,7 +429,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     // of the 32 rows of this warp
     const int first_row = w.row0 + 128 * mt + 32 * (warp & 3);
     const int w_lo = w.past + first_row / a.group, w_hi = w.past + min(first_row + 31, w.all - 1) / a.group;
-    const bool ragged = w.row0 + 128 * mt + 128 > w.all || a.softcap > 0.f;
+    // Rows behind the sequence's last (zero queries) keep a maximum of -infinity, which keeps
+    // their sums out; what they get in P and O is finite and goes nowhere. A warp of them does nothing.
+    const bool idle = first_row >= w.all;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
     // A tile's scales (K's times this row's factor), taken while its scores are still being
     // made: the products keep shared memory busy, and a load waits for hundreds of cycles.
@@ -455,7 +457,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       tc05::fence_after_sync();
       const uint32_t t_s = tmem + lanes + slot * kT;
       const int jt = w.j0 + i * kT;
-      const bool special = ragged || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
+      const bool special = a.softcap > 0.f || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
       const float2* group_scales = s_scales[tick % P::kSlots].group;
       auto factor = [&](int g) { return fac * group_scales[g].x; };
       // The scores of groups g, g + 1, scaled, and where some row of the warp needs it capped and masked.
@@ -545,7 +547,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // leave 2^-126 of what is masked).
       bool seek = __any_sync(0xffffffffu, live && m == -INFINITY), rise = seek || tile_vmax != vmax;
       bool enough = true;
-      int g0 = 0, seek_to = P::kGroups;
+      int g0 = idle ? P::kGroups : 0, seek_to = P::kGroups;
       while (g0 < P::kGroups) {
         if (rise) {
           if (!(ok = raise(seek ? largest(g0, seek_to, enough) : -INFINITY, 8 * g0))) break;
