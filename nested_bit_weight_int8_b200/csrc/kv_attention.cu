@@ -19,8 +19,8 @@
 // other: one product takes 256 bytes of the cache, and a tile of up to 8 rows
 // wastes nothing on padding. A byte b enters as the fp16 subnormal b 2^-24, which
 // takes one byte permutation per two values and no arithmetic; the offset 128
-// comes out of the sums: scores start at -128 2^-24 sum(q), and one more product
-// sums the probabilities that the outputs' 128 stands against. A query row (bf16)
+// comes out of the sums: scores start at -128 2^-24 sum(q), and outputs take one
+// more product with the constant -128 2^-24. A query row (bf16)
 // is scaled by a power of two to below 2 first, so fp16 holds it exactly down to
 // 2^-24 of the row's largest value. Probabilities are rounded to fp16 (2^-11 of
 // each), with the page's V scale relative to the largest seen folded in before;
@@ -288,13 +288,12 @@ struct Worker {
       }
     }
 
-    float o[NR][kMt][4], ps[NR][4];  // ps: 128 2^-24 times the probabilities' sum
+    float o[NR][kMt][4];
     float m[NR][2], l[NR][2], vmax = kTinyScale, vinv = kPScale / kTinyScale;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       m[r][0] = m[r][1] = -INFINITY;
       l[r][0] = l[r][1] = 0.f;
-      ps[r][0] = ps[r][1] = ps[r][2] = ps[r][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < kMt; ++i)
 #pragma unroll
@@ -434,7 +433,6 @@ struct Worker {
             l[r][e] *= k;
             m[r][e] = x;
             const float kv = k * vr;
-            ps[r][e] *= kv, ps[r][2 + e] *= kv;
 #pragma unroll
             for (int i = 0; i < kMt; ++i) o[r][i][e] *= kv, o[r][i][2 + e] *= kv;
           }
@@ -456,13 +454,19 @@ struct Worker {
           l[r][1] += p1 + p3;
           pf[r][0] = transpose_8x8(f16x2(p0 * ratio, p1 * ratio));
           pf[r][1] = transpose_8x8(f16x2(p2 * ratio, p3 * ratio));
-          mma_f16_16816(ps[r], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, pf[r][0], pf[r][1]);
         }
         const uint32_t vb = sb + gi * S::kGroupBytes + 16 * D;
         // four bytes of four tokens: two m-tiles, values 2 i of their run on rows g, 2 i + 1 on rows g + 8
         auto columns = [&](const uint32_t va, const uint32_t vbw, const uint32_t vc, const uint32_t vd, int mt) {
           const uint32_t x0 = __byte_perm(va, vbw, 0x5140), x1 = __byte_perm(va, vbw, 0x7362);
           const uint32_t y0 = __byte_perm(vc, vd, 0x5140), y1 = __byte_perm(vc, vd, 0x7362);
+          // first -128 2^-24 times the probabilities, for the sums to stay as small as the values
+          // (taken off at the end, 128 times the weights' sum would cost a long cache three bits)
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            mma_f16_16816(o[r][mt], 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, pf[r][0], pf[r][1]);
+            mma_f16_16816(o[r][mt + 1], 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, pf[r][0], pf[r][1]);
+          }
 #pragma unroll
           for (int r = 0; r < NR; ++r)
             mma_f16_16816(o[r][mt], codes_lo(x0), codes_hi(x0), codes_lo(y0), codes_hi(y0), pf[r][0], pf[r][1]);
@@ -501,7 +505,7 @@ struct Worker {
         for (int sh = 4; sh < 32; sh <<= 1) l[r][e] += __shfl_xor_sync(0xffffffffu, l[r][e], sh);
         const int lr = 8 * r + 2 * t + e;
         if (lr >= it.rows) continue;
-        auto value = [&](int i, int half) { return (o[r][i][2 * half + e] - ps[r][e]) * kBack; };
+        auto value = [&](int i, int half) { return o[r][i][2 * half + e] * kBack; };
         if (part) {
           if (g == 0) *reinterpret_cast<float2*>(part + part_rows * d + 2 * lr) = make_float2(m[r][e], l[r][e]);
           float* p = part + lr * d;

@@ -79,9 +79,9 @@ def out_error(out: np.ndarray, mass: np.ndarray, gross: np.ndarray, unit: float,
     """Bound on the bf16 output's error: its own rounding 2^-8 |o|; each
     probability off by e^delta twice (itself and the sum), its exponential
     2^-21, its fp16 rounding 2^-11: of `mass`, the sum of p |v|. The running sums
-    take the byte, code + 128, and then 128 times the probabilities away: 8 u a step
-    of 16 tokens and of the joining, of `gross`, the sum of p (255 + 128) s with s the
-    scale of the value's page. Probabilities below 2^-22 of the running maximum,
+    take 128 times a step's probabilities away and add the bytes, code + 128: 8 u a
+    step of 16 tokens and of the joining, of `gross`, the sum of p (255 + 128) s with s
+    the scale of the value's page, which no partial sum exceeds. Probabilities below 2^-22 of the running maximum,
     which is at most the largest, are fp16 subnormals: half a step there is 2^-25 of
     the factor 2^-8 they stand high, 2^-33 of the largest, a token each, times its
     code and twice `unit`, the largest scale of V (their ratio is taken to it, or to
