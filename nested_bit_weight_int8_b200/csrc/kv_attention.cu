@@ -732,9 +732,8 @@ struct Share {
 };
 Share share_of(int D, int64_t max_new, int group) {
   const int64_t rows = max_new * group;
-  const int e = row_eights(D, group), single = 8 * e > group ? 8 * e : group, few = D == 128 ? 16 : 64;
-  const int all = few > single ? few : single;
-  return rows <= all ? Share{row_eights(D, rows), all} : Share{e, single};
+  const int e = row_eights(D, group), few = D == 128 ? 16 : 64, all = few > 8 * e ? few : 8 * e;
+  return rows <= all ? Share{row_eights(D, rows), all} : Share{e, 8 * e};
 }
 
 template <int D, int NR>

@@ -919,7 +919,13 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     w.start(a, at, B - A);
     int k = 0;
     auto publish = [&](int n) {
-      if (k >= 2 && !wait(&bar.plan_empty[k & 1], ((k >> 1) & 1) ^ 1, kErrWaitEmpty)) return false;
+      // this warp alone waits for whole pieces: up to a thousand times what the others wait for a step
+      if (k >= 2) {
+        bool free = false;
+        for (int i = 0; i < 1000 && !free && !__any_sync(0xffffffffu, *s_abort != 0); ++i)
+          free = __all_sync(0xffffffffu, mbar_wait_bounded(&bar.plan_empty[k & 1], ((k >> 1) & 1) ^ 1, wait_ns));
+        if (!free && !wait(&bar.plan_empty[k & 1], ((k >> 1) & 1) ^ 1, kErrWaitEmpty)) return false;
+      }
       if (lane == 0) {
         s_piece[k & 1] = Piece{w.at.s, w.at.h, w.sq.r0, w.it.row0, w.it.rows, w.sq.n * a.group, w.it.past, w.it.lo, w.it.j0, w.it.j1,
                                n, w.t0, w.t1};

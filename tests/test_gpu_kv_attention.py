@@ -335,6 +335,25 @@ def test_two_streams_and_a_graph_that_sees_new_lengths():
     mq.device_status()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_waits_that_give_up_are_reported_and_the_next_call_is_whole(dim):
+    b = Batch([(200, 300), (1, 500), (3, 40)], 2, dim, 32, seed=27, fill="all")
+    q = queries(b, 4)
+    want = attend(b, 4, q)
+    mq.device_status()
+    mq.debug_set_wait_limit_ns(0)  # every wait gives up at once
+    try:
+        attend(b, 4, q)
+        with pytest.raises(mq.MQError) as e:
+            mq.device_status()
+        assert e.value.status == mq.MQ_ERR_TIMEOUT
+    finally:
+        mq.debug_set_wait_limit_ns(2_000_000_000)
+    out, log = attend(b, 4, q)
+    mq.device_status()
+    assert torch.equal(out, want[0]) and torch.equal(log, want[1])
+
+
 @pytest.mark.parametrize("n", [1, 3, 200])
 def test_pages_before_the_window_may_be_gone(n):
     b = Batch([(n, 700), (min(n, 5), 40)], 2, 64, 16, seed=14, fill="all")
