@@ -13,7 +13,12 @@
 //                          start and outputs at the end
 //   kConv warps          : bytes to fp16 codes, K and V, into swizzled rows of
 //                          shared memory (two buffers each)
-//   one warp             : issues the products (one thread)
+//   one warp             : issues the products
+//   one warp             : plans the CTA's pieces of items ahead of the others
+// 2048 tokens upon as many cached ones of two sequences, 32 query and 8 key/value heads
+// of 128 values: 264 us, 780 TFLOP/s of the pairs that count (11.3 ms in plain torch). A
+// tile of 128 tokens and 256 rows takes 4000 cycles, its products 2100, its softmax 2700:
+// they overlap in part, one row tile's softmax beside the other's products.
 // The codes enter exactly (byte - 128), the page scales where a row's thread needs
 // them: K's multiplies the score, V's goes into the exponent, so that it costs
 // no instruction per score: p' = 2^(s + log2(v_scale / v_max) + 8 - m), and the sum

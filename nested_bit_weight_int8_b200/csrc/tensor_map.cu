@@ -1,4 +1,4 @@
-// Host-side encoding of 2-D TMA tensor maps (through the driver entry point,
+// Host-side encoding of 2-D and 3-D TMA tensor maps (through the driver entry point,
 // so the library does not link libcuda directly), with a small cache keyed by
 // (address, shape, box): a map only encodes where and how to read, so a cached
 // map stays valid for any data later written at the same address.

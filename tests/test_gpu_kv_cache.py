@@ -265,3 +265,38 @@ def test_more_sequences_than_one_round_finds():
     got = q.float().cpu().numpy()
     assert np.all(np.abs(got[:len(places)].reshape(-1, 2, 64) - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol) + 1e-30)
     assert np.all(got[len(places):] == 9.0)
+
+
+def test_pages_behind_the_first_four_gigabytes():
+    # the same calls on a cache whose pages lie behind 2^32 bytes: the same bits
+    seqs = [(3, 300), (200, 400), (1, 1000), (1, 0)]
+    small = Batch(seqs, 8, 128, 128, seed=31)
+    pages = 34000  # of 131072 bytes
+    far = pages - small.k.shape[0] - 1
+    assert far * 131072 > 1 << 32
+    big = [torch.zeros(pages, 8, 128, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros(pages, 8, device=DEV) for _ in range(2)]
+    for t, u in ((big[0], small.k), (big[1], small.v), (scales[0], small.ks), (scales[1], small.vs)):
+        t[far:far + len(u)] = u
+    table = torch.where(small.pages >= 0, small.pages + far, small.pages).contiguous()
+    caches = [(small.cache, small.batch), (mq.KVCache(*big, *scales),
+              mq.KVBatch(small.row_start, small.kv_len, table, small.rows, small.max_new, small.max_len))]
+    qkv = torch.randn(small.rows, 48 * 128, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    rope, results = mq.RopeTable(10000.0, 128, device=DEV), []
+    first = torch.zeros(4, dtype=torch.int32, device=DEV)
+    ends = torch.tensor(np.cumsum([0] + [c for _, c in seqs]), dtype=torch.int32, device=DEV)
+    n_out = int(ends[-1])
+    for cache, batch in caches:
+        q, out = (torch.empty(small.rows, 32 * 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        mq.kv_append(cache, batch, qkv[:, 32 * 128:], qkv[:, 40 * 128:], mq.MQ_F32, 48 * 128, 48 * 128, rope=rope, q=qkv,
+                     q_stride=48 * 128, n_q_heads=32, q_out=q)
+        scratch = torch.empty(mq.kv_attention_scratch_bytes(cache, batch, 32), dtype=torch.uint8, device=DEV)
+        mq.kv_attention(cache, batch, q, 32 * 128, 32, 128 ** -0.5, out, 32 * 128, scratch)
+        k, v = (torch.empty(n_out, 8 * 128, device=DEV) for _ in range(2))
+        mq.kv_read(cache, batch, first, ends, n_out, 1000, k, v, mq.MQ_F32, 8 * 128)
+        mq.device_status()
+        results.append((q, out, k, v))
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+    assert torch.equal(big[0][far:far + len(small.k)], small.k) and torch.equal(big[1][far:far + len(small.v)], small.v)
+    assert not torch.any(scales[0][:far]) and not torch.any(scales[0][far + len(small.k):])
