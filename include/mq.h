@@ -455,10 +455,10 @@ MQ_API mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch,
  * h = a / (n_q_heads / n_kv_heads),
  *   s_j = cap(scale q . k_j),  o = sum_j softmax(s)_j v_j,  lse = ln sum_j e^{s_j}
  * over j <= P (and j > P - window if window > 0), cap(s) = softcap
- * tanh(s / softcap) if softcap > 0. A row that sees no token gets o = 0 and
- * lse = -infinity. What pages hold behind kv_len has no part in it, and pages
- * wholly before every row's window are not looked at (their entries may hold
- * anything).
+ * tanh(s / softcap) if softcap > 0 (2^-60 to 2^60). A row that sees no token
+ * gets o = 0 and lse = -infinity. What pages hold behind kv_len has no part in
+ * it, and pages wholly before every row's window are not looked at (their
+ * entries may hold anything).
  *   q, out : n_rows x n_q_heads x head_dim bf16, rows q_stride / out_stride
  *            elements apart (multiples of 8), 16-byte aligned, not overlapping.
  *   lse    : n_rows x n_q_heads fp32, or NULL.

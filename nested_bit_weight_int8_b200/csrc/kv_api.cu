@@ -155,7 +155,8 @@ mq_status kv_attention_args(const char* who, const mq_kv_cache* cache, const mq_
   if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
   if ((st = check_group(who, a.c, a.b, n_q_heads, &a.group)) != MQ_OK) return st;
   if (!std::isfinite(scale)) return refuse(MQ_ERR_INVALID_ARG, "%s: scale must be finite", who);
-  if (!std::isfinite(softcap) || softcap < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: softcap must be finite and >= 0 (0: none)", who);
+  if (!(softcap == 0.f || (softcap >= 0x1p-60f && softcap <= 0x1p60f)))
+    return refuse(MQ_ERR_INVALID_ARG, "%s: softcap must be 0 (none) or in [2^-60, 2^60]", who);
   if (window < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: window must be >= 0 (0: none)", who);
   if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
   if ((st = check_rows(who, "out", out, out_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;

@@ -36,6 +36,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/mq.h"
 #include "kv_internal.h"
@@ -304,7 +305,7 @@ struct Worker {
     // the places of the tile's first and last query token
     const int lo_place = sq.len - sq.n + it.i0;
     const int hi_place = sq.len - sq.n + (first_row + it.rows - 1) / a.group;
-    const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
+    const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     // where this lane's chunks lie in a box: K rows g ^ ((g & 1) << 2) and + 8, V rows 2 t, (2 t + 1) ^ 4 and + 8
     const int krow = g ^ ((g & 1) << 2), va_row = 2 * t, vb_row = (2 * t + 1) ^ 4;
 
@@ -370,22 +371,20 @@ struct Worker {
         for (int gi = 0; gi < S::kGroups; ++gi)
 #pragma unroll
           for (int e = 0; e < 2; ++e) f[r][gi][e] *= 1.f / kCode;
-      if (a.softcap > 0.f) {  // cap tanh(x / cap) = cap - 2 cap / (1 + e^(2 x / cap))
+      auto cap = [&](auto wide) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
           for (int gi = 0; gi < S::kGroups; ++gi) {
-            const float k[2] = {f[r][gi][0] * cap_in, f[r][gi][1] * cap_in};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float y;
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp2_fast(sc[r][gi][e] * k[e & 1])));
-              sc[r][gi][e] = fmaf(-2.f * cap_out, y, cap_out);
-            }
+            for (int e = 0; e < 4; ++e)
+              sc[r][gi][e] = capped<decltype(wide)::value>(sc[r][gi][e] * f[r][gi][e & 1], cap_in, cap_out);
             f[r][gi][0] = f[r][gi][1] = 1.f;
           }
         }
-      }
+      };
+      if (a.softcap > kWideCap) cap(std::true_type{});
+      else if (a.softcap > 0.f) cap(std::false_type{});
       if (masked) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {

@@ -18,10 +18,21 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float tanh_fast(float x) {
-  float r;  // 1 - 2 / (1 + e^2x): within 2^-22 absolutely, which is what a score needs
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(2.f * kLog2e * x)));
-  return fmaf(-2.f, r, 1.f);
+// cap tanh(s / cap), base 2, from s, 1 / cap and cap log2(e): 1 - 2 / (1 + e^2x) is within
+// 2^-22 absolutely, so 2^-22 cap; where that is much (kWideCap), scores below cap / 16 take the
+// series x - x^3 / 3 + 2 x^5 / 15 (2^-28 there) and keep their own precision.
+constexpr float kWideCap = 64.f;
+template <bool WIDE>
+__device__ __forceinline__ float capped(float score, float inverse, float cap_log2e) {
+  const float x = score * inverse;
+  float t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(1.f + exp2_fast(2.f * kLog2e * x)));
+  t = fmaf(-2.f, t, 1.f);
+  if constexpr (WIDE) {
+    const float z = x * x;
+    if (fabsf(x) < 0.0625f) t = x * fmaf(z, fmaf(z, 2.f / 15.f, -1.f / 3.f), 1.f);
+  }
+  return cap_log2e * t;
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

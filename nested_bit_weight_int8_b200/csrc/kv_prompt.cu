@@ -474,7 +474,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * (e < 16 ? f0 : f1));
         if (a.softcap > 0.f) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(cap_out * tanh_fast(__uint_as_float(v[e]) * cap_in));
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(capped<true>(__uint_as_float(v[e]), cap_in, cap_out));
         }
         if (special) {
           const int hi = place - jt - 16 * g, low = a.window > 0 ? hi - a.window : -1;

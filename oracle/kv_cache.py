@@ -67,12 +67,14 @@ def score_error(q: np.ndarray, unit: float, scale: float, softcap: float) -> np.
     -128 sum(q): no partial sum exceeds 255 unit |q|_1, and each of the dim / 16
     + 16 steps (a tensor core may cut a step by 2 u of that) and of the dim / 4 + 4
     additions of sum(q) costs of it; the scalings 6 u. For the cap 4 u of its range,
-    twice. u = 2^-24. A query's values below 2^-25 of its largest are lost:
-    2^-25 dim 127 unit |q|max."""
+    twice, or, of scores below a sixteenth of it where it is wide (above 64), 8 u of
+    themselves, so never more than 8 u 16 |score|. u = 2^-24. A query's values below
+    2^-25 of its largest are lost: 2^-25 dim 127 unit |q|max."""
     u, dim = 2.0 ** -24, q.shape[1]
     big = 255 * unit * np.sum(np.abs(q), axis=1)
     lost = 2.0 ** -25 * dim * np.max(np.abs(q), axis=1) * 127 * unit
-    return abs(scale) * (big * (2 * (dim / 16 + 16) + dim / 4 + 4 + 6) * u + lost) + (8 * u * softcap)
+    cap = np.minimum(softcap, 16 * abs(scale) * big) if softcap > 64 else softcap
+    return abs(scale) * (big * (2 * (dim / 16 + 16) + dim / 4 + 4 + 6) * u + lost) + 8 * u * cap
 
 
 def out_error(out: np.ndarray, mass: np.ndarray, gross: np.ndarray, unit: float, delta: np.ndarray, tokens: int) -> np.ndarray:
@@ -82,13 +84,13 @@ def out_error(out: np.ndarray, mass: np.ndarray, gross: np.ndarray, unit: float,
     take 128 times a step's probabilities away and add the bytes, code + 128: 8 u a
     step of 16 tokens and of the joining, of `gross`, the sum of p (255 + 128) s with s
     the scale of the value's page, which no partial sum exceeds. Probabilities below 2^-22 of the running maximum,
-    which is at most the largest, are fp16 subnormals: half a step there is 2^-25 of
-    the factor 2^-8 they stand high, 2^-33 of the largest, a token each, times its
-    code and twice `unit`, the largest scale of V (their ratio is taken to it, or to
-    the power of two above it)."""
+    which is at most the largest or the integer (base 2) above it, are fp16 subnormals:
+    half a step there is 2^-25 of the factor 2^-8 they stand high, 2^-33 of twice the
+    largest, a token each, times its code and twice `unit`, the largest scale of V (their
+    ratio is taken to it, or to the power of two above it)."""
     u = 2.0 ** -24
     rel = 2 * np.expm1(delta)[:, None] + 2.0 ** -20 + 2.0 ** -11
-    under = tokens * 2.0 ** -33 * 127 * 2 * unit
+    under = tokens * 2.0 ** -33 * 127 * 4 * unit
     return (2.0 ** -8 * np.abs(out) + rel * mass + 8 * u * (tokens / 16 + 32) * gross[:, None] + under) * (1 + 2.0 ** -8)
 
 

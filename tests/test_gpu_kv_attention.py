@@ -157,6 +157,16 @@ def test_scales_of_either_sign(seqs, scale):
         check(b, 4, q, out, log, softcap=cap, scale=scale)
 
 
+@pytest.mark.parametrize("cap", [0.01, 64.0, 100.0, 5000.0, 1e6, 2.0 ** 60])
+def test_narrow_and_wide_caps(cap):
+    b = Batch([(200, 300), (3, 200), (1, 17)], 1, 128, 32, seed=28, fill="all")
+    for size in (0.01, 2.0):
+        q = queries(b, 2, size=size)
+        out, log = attend(b, 2, q, softcap=cap)
+        mq.device_status()
+        check(b, 2, q, out, log, softcap=cap)
+
+
 @pytest.mark.parametrize("dim", [64, 256])
 def test_nan_and_infinite_queries_stay_in_their_rows_of_a_prompt(dim):
     b = Batch([(300, 350), (1, 9)], 1, dim, 16, seed=25, fill="all")

@@ -75,7 +75,8 @@ def test_read_refuses(kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), BAD), (dict(q=F + 8), BAD), (dict(qs=1020), BAD), (dict(qs=1000), BAD), (dict(hq=7), BAD), (dict(hq=0), BAD),
-    (dict(hq=1), BAD), (dict(scale=math.nan), BAD), (dict(cap=-1.0), BAD), (dict(cap=math.inf), BAD), (dict(window=-1), BAD),
+    (dict(hq=1), BAD), (dict(scale=math.nan), BAD), (dict(cap=-1.0), BAD), (dict(cap=math.inf), BAD), (dict(cap=2.0 ** -61), BAD),
+    (dict(cap=2.0 ** 61), BAD), (dict(cap=math.nan), BAD), (dict(window=-1), BAD),
     (dict(out=None), BAD), (dict(os=1023), BAD), (dict(lse=F + 2), BAD), (dict(scr=None), BAD), (dict(scr=F + 128), BAD),
     (dict(size=64), BAD), (dict(hq=32768, qs=1 << 23, os=1 << 23), NOT_SERVED)])
 def test_attention_refuses(kw, want):
