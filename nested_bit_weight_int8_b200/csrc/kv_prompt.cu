@@ -47,6 +47,11 @@ namespace mq {
 namespace {
 
 constexpr float kPLog2 = 8.f;          // p' stands 2^8 high
+// Rows whose maximum lies beyond this form an exponent from the rounded score, the maximum
+// taken off before the scale's logarithm comes on: together, the logarithm would lose up to
+// half a step of the maximum (2^-13 here), and the score, not rounded as the maximum's was,
+// could stand above it by as much again: at 2^27 a weight of 2^8 for the largest.
+constexpr float kCoarse = 0x1p12f;
 constexpr float kTinyScale = 0x1p-100f;  // V scales below this count as this
 
 // Two bytes of a word as the fp16 pair of byte - 128: 0x6400 | byte is 1024 + byte.
@@ -438,6 +443,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     // their sums out; what they get in P and O is finite and goes nowhere. A warp of them does nothing.
     const bool idle = first_row >= w.all;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
+    bool coarse = false;  // some row of this warp has a maximum beyond kCoarse
     // A tile's scales (K's times this row's factor), taken while its scores are still being
     // made: the products keep shared memory busy, and a load waits for hundreds of cycles.
     float fs[P::kGroups], lg[P::kGroups], tile_vmax = 0.f;
@@ -509,6 +515,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         l *= k;
         sum *= k;
         m = x;
+        coarse = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m) >= kCoarse);
         vmax = tile_vmax;
         const __half2 k2 = __float2half2_rn(k);
         tc05::wait_st();  // P so far
@@ -550,17 +557,21 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // The special-function unit would take 2048 cycles of 256 rows' tile, as the products
       // do; every fourth pair of exponentials goes to the multiply-add pipes instead (which
       // leave 2^-126 of what is masked).
-      bool seek = __any_sync(0xffffffffu, live && m == -INFINITY), rise = seek || tile_vmax != vmax;
-      bool enough = true;
-      int g0 = idle ? P::kGroups : 0, seek_to = P::kGroups;
+      // A step is done over once at most: the maximum is then at least that of its own scores
+      // and no p' stands above 2^8 (but for the roundings below kCoarse), no group's sum above
+      // 2^12. Tiles with a maximum beyond kCoarse go the way of the masked ones, to their end.
+      const bool first = __any_sync(0xffffffffu, live && m == -INFINITY);
+      bool rise = first || tile_vmax != vmax, enough = true, careful = special || coarse;
+      int g0 = idle ? P::kGroups : 0, seek_to = first ? P::kGroups : 0;  // where a maximum is looked for ends
       while (g0 < P::kGroups) {
         if (rise) {
-          if (!(ok = raise(seek ? largest(g0, seek_to, enough) : -INFINITY, 8 * g0))) break;
-          rise = enough = false;
+          if (!(ok = raise(largest(g0, seek_to, enough), 8 * g0))) break;
+          rise = false;
+          careful |= coarse;
         }
         const float m0 = m == -INFINITY ? 0.f : m;
         float part = 0.f, big = 0.f;
-        auto group = [&](const uint32_t* x, float f, float lg, uint32_t* pk) {
+        auto group = [&](const uint32_t* x, float f, float lg, float m0, uint32_t* pk) {
           const uint64_t f2 = pair(f, f), c2 = pair(lg - m0, lg - m0);
           uint64_t s0 = 0, s1 = 0;
 #pragma unroll
@@ -579,27 +590,29 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           part = fmaf(t.x + t.y, exp2_fast(-lg), part);
         };
         int step;
-        if (!special) {
+        if (!careful) {
           step = 4;
           uint32_t v[2][32], pk[32];
           tc05::ld_32x32b_x32(t_s + 16 * g0, v[0]);
           tc05::ld_32x32b_x32(t_s + 16 * g0 + 32, v[1]);
           tc05::wait_ld();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), fs[g], lg[g], pk + 8 * g);
-          rise = __any_sync(0xffffffffu, big > 32768.f);
+          for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), fs[g], lg[g], m0, pk + 8 * g);
+          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f);
           if (!rise) tc05::st_32x32b_x32(t_s + 8 * g0, pk);
         } else {
           step = 2;
           uint32_t v[32], pk[16];
           scores(v, g0);
-          group(v, 1.f, group_scales[g0].y, pk);
-          group(v + 16, 1.f, group_scales[g0 + 1].y, pk + 8);
-          rise = __any_sync(0xffffffffu, big > 32768.f);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - m0);  // see kCoarse
+          group(v, 1.f, group_scales[g0].y, 0.f, pk);
+          group(v + 16, 1.f, group_scales[g0 + 1].y, 0.f, pk + 8);
+          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f);
           if (!rise) tc05::st_32x32b_x16(t_s + 8 * g0, pk);
         }
-        if (rise) {
-          seek = true;
+        if (rise) {  // done over, with the maximum of all its scores
+          enough = false;
           seek_to = g0 + step;
         } else {
           sum += part;
