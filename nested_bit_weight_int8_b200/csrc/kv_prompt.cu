@@ -82,9 +82,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x of two values on the multiply-add pipes, for x in [-126, 128): 2^round(x) times a
+// 2^x of two values on the multiply-add pipes, for x in [-126, 127]: 2^round(x) times a
 // polynomial of degree 5 in the rest, |rest| <= 1/2, whose coefficients make the largest
-// relative error smallest (2^-23.7; 2^-22.2 in fp32). Below -126 it gives 2^-126.
+// relative error smallest (2^-23.7; 2^-22.2 in fp32). Below -126, and for a NaN, it gives
+// 2^-126. Above 127 the exponent runs into the sign: the caller looks out for such x.
 __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
   const float2 v = unpair(x);
   const uint64_t y = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
@@ -549,7 +550,8 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       };
       // p' of 64 tokens at a time (32 where they are masked), over scores that are read
       // already. The running maximum is not looked for: a score that passes it by more than
-      // 6 or so shows in its group's sum, and its step is done over. Rows that have seen
+      // 6 or so shows in its group's sum (or, as the polynomial's sums hold for small x only,
+      // in the largest of those: half the price of a clamp), and its step is done over. Rows that have seen
       // nothing yet take a maximum first, of the tokens up to the first they see. Without branches within a step, for its
       // loads, exponentials and sums to mix, and rolled up, for the code to stay in the
       // instruction cache beside the other warps': unrolled over the tile, fetches were the
@@ -570,7 +572,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           careful |= coarse;
         }
         const float m0 = m == -INFINITY ? 0.f : m;
-        float part = 0.f, big = 0.f;
+        float part = 0.f, big = 0.f, over = 0.f;
         auto group = [&](const uint32_t* x, float f, float lg, float m0, uint32_t* pk) {
           const uint64_t f2 = pair(f, f), c2 = pair(lg - m0, lg - m0);
           uint64_t s0 = 0, s1 = 0;
@@ -580,6 +582,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
             const float2 y = unpair(y2), z = unpair(x2);
             const float2 p = make_float2(exp2_fast(z.x), exp2_fast(z.y));
             const float2 q = e % 8 == 4 ? exp2_poly(y2) : make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            if (e % 8 == 4) over = fmaxf(over, fmaxf(y.x, y.y));
             s0 = add2(s0, pair(p.x, p.y));
             s1 = add2(s1, pair(q.x, q.y));
             pk[e / 2] = f16x2(p.x, p.y);
@@ -598,7 +601,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           tc05::wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g) group(v[g / 2] + 16 * (g & 1), fs[g], lg[g], m0, pk + 8 * g);
-          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f);
+          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f || over > 15.f);
           if (!rise) tc05::st_32x32b_x32(t_s + 8 * g0, pk);
         } else {
           step = 2;
@@ -608,7 +611,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - m0);  // see kCoarse
           group(v, 1.f, group_scales[g0].y, 0.f, pk);
           group(v + 16, 1.f, group_scales[g0 + 1].y, 0.f, pk + 8);
-          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f);
+          rise = (enough || g0 >= seek_to) && __any_sync(0xffffffffu, big > 32768.f || over > 15.f);
           if (!rise) tc05::st_32x32b_x16(t_s + 8 * g0, pk);
         }
         if (rise) {  // done over, with the maximum of all its scores

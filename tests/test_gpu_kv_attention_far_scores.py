@@ -73,3 +73,59 @@ def test_prompts_of_very_large_scores(power, dim, group, window, softcap):
     out, log = attend(b, group, q, softcap=softcap, window=window, scale=1.0)
     mq.device_status()
     check_equal_scores(b, group, q, out, log, window, softcap)
+
+
+def one_far_key(dim, n, held, seed, places, low):
+    """Sequences of n rows upon `held` tokens; sequence i's key at places[i] is 127 in every value, all
+    others are `low`."""
+    b = Batch([(n, held + n)] * len(places), 1, dim, 32, seed=seed, fill="all")
+    b.codes[0][:] = 128 + low
+    for i, p in enumerate(places):
+        b.codes[0][b.table[i, p // 32], 0, p % 32] = 255
+    b.scales[0][:] = 1.0
+    for t, c in ((b.k, b.codes[0]), (b.ks, b.scales[0])):
+        t.copy_(torch.from_numpy(c))
+    return b
+
+
+def check_far_key(b, q, out, log, scale, softcap):
+    """The others' scores are one number, and what stands next to the far key weighs 2^-90 at most: scores
+    add no error to the outputs, 8 u of themselves and of the cap to the lse. All sequences at once."""
+    (n, c), seqs, u = b.seqs[0], len(b.seqs), 2.0 ** -24
+    pages = b.pages[:, :-(-c // b.page)].long()
+    k, v = (((t[pages, 0].reshape(seqs, -1, b.dim)[:, :c].double() - 128) * s) for t, s in (
+        (b.k, b.ks[pages, 0].double().repeat_interleave(b.page, 1)[:, :c, None]),
+        (b.v, b.vs[pages, 0].double().repeat_interleave(b.page, 1)[:, :c, None])))
+    score = q.double().view(seqs, n, b.dim) @ k.transpose(1, 2) * scale
+    if softcap:
+        score = softcap * torch.tanh(score / softcap)
+    score = score.masked_fill(torch.ones(n, c, dtype=torch.bool, device=DEV).triu(c - n + 1), -torch.inf)
+    p, l = score.softmax(-1), score.logsumexp(-1).flatten().cpu().numpy()
+    o, mass = ((p @ x).view(-1, b.dim).cpu().numpy() for x in (v, v.abs()))
+    gross = (p @ b.vs[pages, 0].double().repeat_interleave(b.page, 1)[:, :c, None]).flatten().cpu().numpy() * 383
+    err = np.abs(out.float().cpu().numpy() - o)
+    tol = okv.out_error(o, mass, gross, float(b.vs.max()), np.zeros(b.rows), c)
+    assert np.all(err <= tol), [(r // n, r % n) for r in np.unique(np.argwhere(~(err <= tol))[:, 0])[:8]]
+    assert np.all(np.abs(log.double().cpu().numpy()[:, 0] - l) <= okv.lse_error(l, 8 * u * (np.abs(l) + softcap), c))
+
+
+# gaps in base 2
+@pytest.mark.parametrize("gap,softcap", [(g, 0.0) for g in (90, 118, 120, 125, 130, 140, 200, 254, 400, 600)] +
+                         [(g, 200.0) for g in (90, 120, 125, 130, 200)] + [(140, 50.0)])
+@pytest.mark.parametrize("dim,n", [(64, 100), (64, 150), (128, 100), (128, 150), (256, 100)])
+def test_prompts_with_one_far_outweighing_key(dim, n, gap, softcap):
+    held = 260
+    # each place of 64 in turn: behind the first 32 tokens, in a later tile, among the masked
+    for seed, start in enumerate((32, 160, held)):
+        b = one_far_key(dim, n, held, seed, [start + i for i in range(64)], -127 if softcap == 50.0 else 0)
+        size = gap * np.log(2) if softcap != 50.0 else gap * np.log(2) / 2  # of the far key's score; -size of the others then
+        scale = (softcap * np.arctanh(size / softcap) if softcap else size) / (127 * dim)
+        for rows in ("all", "one"):
+            q = torch.zeros(b.rows, dim, device=DEV, dtype=torch.bfloat16)
+            if rows == "all":
+                q[:] = 1
+            else:  # the last row of each sequence, alone in its warp: no other's sum tells of the step
+                q[torch.from_numpy(b.starts[1:] - 1).to(DEV)] = 1
+            out, log = attend(b, 1, q, softcap=softcap, scale=float(np.float32(scale)))
+            mq.device_status()
+            check_far_key(b, q, out, log, float(np.float32(scale)), softcap)
