@@ -293,6 +293,7 @@ struct Worker {
 
     float o[NR][kMt][4];
     float m[NR][2], l[NR][2], vmax = kTinyScale, vinv = kPScale / kTinyScale;
+    bool coarse = false;  // some row has a maximum beyond kCoarse
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       m[r][0] = m[r][1] = -INFINITY;
@@ -364,7 +365,7 @@ struct Worker {
       }
       // ---- cap and mask, where there is one; a score (base 2) is then sc f
       const int jt = it.j0 + tile * S::kTile;
-      const bool masked = dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
+      const bool masked = coarse || dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -418,11 +419,12 @@ struct Worker {
 #pragma unroll
           for (int gi = 1; gi < S::kGroups; ++gi) x = fmaxf(x, fmaxf(sc[r][gi][e], sc[r][gi][2 + e]) * f[r][gi][e]);
           top[r][e] = x;
-          grew |= x > m[r][e] + kSlack;
+          grew |= x - m[r][e] > kSlack;  // (not m + kSlack, which may round up)
         }
       }
       if (__any_sync(0xffffffffu, grew)) {
         const float vr = vmax / vnew;
+        bool far = false;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
@@ -433,9 +435,22 @@ struct Worker {
             const float k = x == -INFINITY ? 1.f : exp2_fast(m[r][e] - x);
             l[r][e] *= k;
             m[r][e] = x;
+            far |= x != -INFINITY && fabsf(x) >= kCoarse;
             const float kv = k * vr;
 #pragma unroll
             for (int i = 0; i < kMt; ++i) o[r][i][e] *= kv, o[r][i][2 + e] *= kv;
+          }
+        }
+        coarse = __any_sync(0xffffffffu, far);
+        if (coarse) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+#pragma unroll
+            for (int gi = 0; gi < S::kGroups; ++gi) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[r][gi][e] *= f[r][gi][e & 1];
+              f[r][gi][0] = f[r][gi][1] = 1.f;
+            }
           }
         }
         vmax = vnew;

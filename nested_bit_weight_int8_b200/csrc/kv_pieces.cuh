@@ -34,6 +34,12 @@ __device__ __forceinline__ float capped(float score, float inverse, float cap_lo
   }
   return cap_log2e * t;
 }
+// Rows whose maximum lies beyond this form a weight's exponent from the rounded score, the
+// maximum taken off before anything else comes on. Score times factor less maximum in one
+// rounding is finer, but keys of one score then differ by up to half a step of it between
+// tiles that are masked and others, and from 2^25 on a weight passes what fp16 holds. The
+// logarithm of a V scale, added to a maximum first, would lose as much.
+constexpr float kCoarse = 0x1p12f;  // half a step: 2^-13
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

@@ -47,11 +47,6 @@ namespace mq {
 namespace {
 
 constexpr float kPLog2 = 8.f;          // p' stands 2^8 high
-// Rows whose maximum lies beyond this form an exponent from the rounded score, the maximum
-// taken off before the scale's logarithm comes on: together, the logarithm would lose up to
-// half a step of the maximum (2^-13 here), and the score, not rounded as the maximum's was,
-// could stand above it by as much again: at 2^27 a weight of 2^8 for the largest.
-constexpr float kCoarse = 0x1p12f;
 constexpr float kTinyScale = 0x1p-100f;  // V scales below this count as this
 
 // Two bytes of a word as the fp16 pair of byte - 128: 0x6400 | byte is 1024 + byte.
