@@ -418,7 +418,9 @@ typedef struct mq_kv_batch {
  * Per page and head, with m = max |x| over the tokens the call adds to it:
  *   s' = max(s, m / 127)   (s = 0 for a page that held no token before),
  *   held codes c -> rint(c s / s') where s' > s,   new codes rint(x / s'),
- * every operation IEEE binary32, correctly rounded (x after rotation in fp32).
+ * every operation IEEE binary32, correctly rounded (x after rotation in fp32),
+ * codes kept within [-127, 127] (a subnormal s' may be rounded below m / 127;
+ * a page whose largest value is below 64 steps of 2^-149 gets the scale 0).
  * A call that repeats tokens writes the same bytes again.
  *   k, v : n_rows x n_kv_heads x head_dim (MQ_F32 or MQ_BF16), rows k_stride /
  *          v_stride elements apart (a multiple of 4), aligned to 4 elements;

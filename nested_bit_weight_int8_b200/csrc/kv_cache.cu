@@ -222,7 +222,7 @@ __device__ __forceinline__ bool find_place(const KvBatch& b, int row, int lane, 
   return true;
 }
 
-// rint(x / s) + 128 in the low byte, x / s correctly rounded: with r = 1 / s correctly
+// rint(x / s) + 128 in the low byte, within [-127, 127] + 128, x / s correctly rounded: with r = 1 / s correctly
 // rounded and q = x r, the remainder x - q s is exact and q + r (x - q s) rounds as x / s
 // does (Markstein, IBM J. Res. Dev. 34, 1990). That needs the remainder to be above the
 // subnormals where it matters, |x / s| > 1/4: a scale of 2^-100 does. Four operations a value
@@ -240,7 +240,8 @@ struct Coder {
   template <bool TINY>
   __device__ __forceinline__ uint32_t one(float x) const {
     float q = x * r;
-    q = TINY ? __fdiv_rn(x, s) : fmaf(fmaf(-q, s, x), r, q);
+    // (a subnormal scale is rounded by up to half of itself, so a quotient may pass 127)
+    q = TINY ? fminf(fmaxf(__fdiv_rn(x, s), -127.f), 127.f) : fmaf(fmaf(-q, s, x), r, q);
     return __float_as_uint(q + 12583040.f);  // 1.5 2^23 + 128: rounds to an integer, ties to even
   }
   template <bool TINY>
