@@ -290,11 +290,11 @@ mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const i
   a.first = first;
   a.out_start = out_start;
   a.n_out = static_cast<int>(n_out);
-  a.max_out = static_cast<int>(max_out < a.b.max_len ? max_out : a.b.max_len);
+  a.max_out = static_cast<int>(max_out);
   a.k_out = k_out;
   a.v_out = v_out;
   a.out_stride = out_stride;
-  if (a.max_out == 0) return MQ_OK;
+  if (a.b.max_len == 0) return MQ_OK;
   cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
   return finish(launch_kv_read(a, dtype, static_cast<cudaStream_t>(stream)), who);

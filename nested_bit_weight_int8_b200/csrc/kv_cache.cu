@@ -525,7 +525,9 @@ cudaError_t launch_kv_append(const AppendArgs& a, int dtype, cudaStream_t stream
 }
 
 cudaError_t launch_kv_read(const ReadArgs& a, int dtype, cudaStream_t stream) {
-  const int slots = (a.max_out + a.c.page - 2) / a.c.page + 1;
+  // rows behind a sequence's tokens are not written: max_len bounds the pages of any
+  const int tokens = a.max_out < a.b.max_len ? a.max_out : a.b.max_len;
+  const int slots = (tokens + a.c.page - 2) / a.c.page + 1;
   if (a.c.heads * 2 > 65535 || a.b.n_seqs > 65535) return cudaErrorNotSupported;
   const dim3 g(slots, a.c.heads * 2, a.b.n_seqs);
   if (dtype == MQ_F32) return launch_pdl(kv_read_kernel<float>, g, dim3(kReadThreads), 0, stream, a);

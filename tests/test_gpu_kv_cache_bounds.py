@@ -52,3 +52,36 @@ def test_codes_stay_in_range_on_pages_of_subnormal_values(held):
             assert np.array_equal(scales[mine, 0], scale)
             assert np.array_equal(codes[mine, 0, held:].astype(int) - 128, want.astype(int))
             assert np.array_equal(codes[mine, 0, :held].astype(int) - 128, before.astype(int))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_read_back_of_more_rows_than_the_batch_has_tokens(dtype):
+    # rows at or behind kv_len are left as they were, however many of them are asked for
+    heads, dim, page = 2, 64, 32
+    seqs, counts, first = [(1, 64), (1, 33), (1, 0)], [100, 64, 70], [0, 20, 0]
+    b = Batch(seqs, heads, dim, page, seed=3, fill="all")
+    assert max(counts) > b.max_len
+    ends = np.cumsum([0] + counts)
+    k, v = (torch.full((int(ends[-1]), heads * dim), 5.0, device=DEV, dtype=dtype) for _ in range(2))
+    mq.kv_read(b.cache, b.batch, torch.tensor(first, dtype=torch.int32, device=DEV),
+               torch.tensor(ends, dtype=torch.int32, device=DEV), int(ends[-1]), max(counts), k, v,
+               mq.MQ_F32 if dtype == torch.float32 else mq.MQ_BF16, heads * dim)
+    mq.device_status()
+    for which, got in ((0, k), (1, v)):
+        want = np.full((int(ends[-1]), heads, dim), 5.0, dtype=np.float32)
+        for s, (_, c) in enumerate(seqs):
+            for h in range(heads if c else 0):
+                codes, scales = b.tokens(which, s, h, c)
+                x = codes.astype(np.float32) * np.repeat(scales, page)[:c, None]
+                want[ends[s]:ends[s] + c - first[s], h] = x[first[s]:]
+        assert torch.equal(got.cpu(), torch.from_numpy(want).to(dtype).view(got.shape))
+
+
+def test_read_back_of_more_rows_than_max_out_is_reported():
+    b = Batch([(1, 64)], 1, 64, 32, seed=3, fill="all")
+    k, v = (torch.full((100, 64), 5.0, device=DEV) for _ in range(2))
+    zero, ends = (torch.tensor(t, dtype=torch.int32, device=DEV) for t in ([0], [0, 50]))
+    mq.kv_read(b.cache, b.batch, zero, ends, 100, 49, k, v, mq.MQ_F32, 64)
+    with pytest.raises(mq.MQError) as e:
+        mq.device_status()
+    assert e.value.status == mq.MQ_ERR_BOUNDS and torch.all(k == 5.0) and torch.all(v == 5.0)
