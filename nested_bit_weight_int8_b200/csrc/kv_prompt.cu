@@ -620,7 +620,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         }
       }
       if (!ok) break;
-      if (m != -INFINITY) l += sum;
+      if (m != -INFINITY || sum != sum) l += sum;  // a NaN is passed on, though it is no maximum
       tc05::wait_st();
       // A wait on a barrier tells a phase from the one before it only, so no warp may leave a
       // tile's products further behind. Two tiles of rows: the scores came after them. S twice

@@ -155,3 +155,19 @@ def test_few_rows_with_one_far_outweighing_key(dim, n, gap, softcap):
         out, log = attend(b, 1, q, softcap=softcap, scale=scale)
         mq.device_status()
         check_far_key(b, q, out, log, scale, softcap, small=gap < 90)
+
+
+@pytest.mark.parametrize("seqs", [[(3, 200), (1, 17)], [(90, 500), (200, 300)]])
+@pytest.mark.parametrize("dim,window", [(64, 0), (128, 50), (256, 0)])
+def test_a_query_that_is_no_number_gives_no_number(seqs, dim, window):
+    # outputs and lse alike, in its row and head alone; -infinity is for rows that see nothing
+    b = Batch(seqs, 1, dim, 32, seed=29, fill="all")
+    q = torch.randn(b.rows, 2 * dim, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(torch.bfloat16)
+    bad = torch.zeros(b.rows, 2, dtype=torch.bool, device=DEV)
+    for row in (0, int(b.starts[1]) - 1, int(b.starts[2]) - 1):
+        q[row, dim + row % dim] = float("nan")
+        bad[row, 1] = True
+    out, log = attend(b, 2, q, window=window)
+    mq.device_status()
+    assert torch.equal(torch.isnan(log), bad)
+    assert torch.equal(torch.isnan(out).view(b.rows, 2, dim), bad[:, :, None].expand(-1, -1, dim))
