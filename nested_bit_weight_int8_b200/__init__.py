@@ -275,7 +275,7 @@ class ChainPlan:
         (n_rows x D fp32) in place. scratch: decode_scratch_bytes."""
         if self.caches is None:
             raise ValueError("the plan has no caches")
-        _check(_chain_decode(self.arr, self.cache_arr, self.n, batch.desc, rope.desc if rope is not None else None,
+        _check(_chain_decode(self.arr, self.cache_arr, self.n, batch.desc, _table(rope),
                              softcap, window, self.D, self.Dkv, self.F, _ptr(h), _ptr(scratch),
                              scratch.numel() * scratch.element_size(), MQ_CHAIN_GRAPH if graph else 0, _stream(stream)))
 
@@ -292,7 +292,8 @@ class RopeTable:
     """Rotary positions for heads of which the first rot_dim values turn:
     base theta, layout "half" or "interleaved", scaling "plain", "linear"
     (params: factor), "bands" (factor, low, high, original length) or "yarn"
-    (factor, beta fast, beta slow, original length). Holds the device table."""
+    (factor, beta fast, beta slow, original length). Holds the table on `device`;
+    without one it stays on the host, for inspection, and the calls refuse it."""
 
     def __init__(self, theta: float, rot_dim: int, layout: str = "half", scaling: str = "plain",
                  params=(), device=None):
@@ -307,6 +308,14 @@ class RopeTable:
         self.turns = host if device is None else host.to(device)
         self.factor = factor.value
         self.desc = RopePositions(self.turns.data_ptr(), rot_dim, ROPE_LAYOUTS[layout], factor.value)
+
+
+def _table(rope: RopeTable | None):
+    if rope is None:
+        return None
+    if not rope.turns.is_cuda:
+        raise ValueError("the rope table lies on the host: give RopeTable a CUDA device")
+    return rope.desc
 
 
 class KVCache:
@@ -345,7 +354,7 @@ class KVBatch:
 def rope(x, x_dtype: int, n_rows: int, n_heads: int, head_dim: int, x_stride: int, positions, table: RopeTable,
          y, y_dtype: int, y_stride: int, stream=None) -> None:
     """Rotary positions of n_rows x n_heads heads; y may be x. Strides in elements."""
-    _check(_rope(_ptr(x), x_dtype, n_rows, n_heads, head_dim, x_stride, _ptr(positions), table.desc, _ptr(y),
+    _check(_rope(_ptr(x), x_dtype, n_rows, n_heads, head_dim, x_stride, _ptr(positions), _table(table), _ptr(y),
                  y_dtype, y_stride, _stream(stream)))
 
 
@@ -355,7 +364,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, dtype: int, k_stride: int, v
     """Quantises the batch's new keys (rotated) and values into the cache, and
     writes their rotated queries to q_out (bf16) if q is given."""
     _check(_kv_append(cache.desc, batch.desc, _ptr(k), _ptr(v), dtype, k_stride, v_stride,
-                      rope.desc if rope is not None else None, _ptr(positions), _ptr(q), q_stride, n_q_heads,
+                      _table(rope), _ptr(positions), _ptr(q), q_stride, n_q_heads,
                       _ptr(q_out), _stream(stream)))
 
 

@@ -187,3 +187,18 @@ def test_chain_decode_scratch_bytes():
         plan.decode_scratch_bytes(None)
     with pytest.raises(ValueError):
         mq.ChainPlan([], 1, 512, 256, 1024, 128, caches=[None])
+
+
+def test_a_rope_table_on_the_host_is_refused_by_every_call():
+    # without a device the table is for inspection: no kernel gets a host address
+    table, t = mq.RopeTable(10000.0, 128), torch.zeros(16)
+    assert not table.turns.is_cuda
+    codes, scales = torch.zeros(4, 2, 16, 128, dtype=torch.uint8), torch.zeros(4, 2)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    c, b = mq.KVCache(codes, codes, scales, scales), mq.KVBatch(i(3), i(2), i(2, 4), 2, 1, 8)
+    plan = mq.ChainPlan([], 1, 512, 256, 1024, 128, caches=[])
+    for fn in (lambda: mq.rope(t, mq.MQ_F32, 1, 1, 16, 16, i(1), table, t, mq.MQ_F32, 16),
+               lambda: mq.kv_append(c, b, t, t, mq.MQ_F32, 256, 256, rope=table),
+               lambda: plan.decode(b, t, t, rope=table)):
+        with pytest.raises(ValueError, match="host"):
+            fn()
