@@ -324,10 +324,11 @@ class KVCache:
     fp32, all dense. The descriptor is marshalled once."""
 
     def __init__(self, k, v, k_scale, v_scale):
+        import torch
         pages, heads, page, dim = k.shape
-        for t, shape, item in ((k, k.shape, 1), (v, k.shape, 1), (k_scale, (pages, heads), 4),
-                               (v_scale, (pages, heads), 4)):
-            if tuple(t.shape) != tuple(shape) or t.element_size() != item or not t.is_contiguous():
+        for t, shape, dtype in ((k, k.shape, torch.uint8), (v, k.shape, torch.uint8),
+                                (k_scale, (pages, heads), torch.float32), (v_scale, (pages, heads), torch.float32)):
+            if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("cache tensors must be dense: codes (pages, heads, page, dim) uint8, "
                                  "scales (pages, heads) fp32")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
@@ -341,9 +342,10 @@ class KVBatch:
     and max_len bound the rows and tokens of any sequence."""
 
     def __init__(self, row_start, kv_len, page_table, n_rows: int, max_new: int, max_len: int):
+        import torch
         seqs = kv_len.shape[0]
         for t, shape in ((row_start, (seqs + 1,)), (kv_len, (seqs,)), (page_table, (seqs, page_table.shape[-1]))):
-            if tuple(t.shape) != shape or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+            if tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError("batch tensors must be dense int32: row_start (seqs + 1), kv_len (seqs), "
                                  "page_table (seqs, pages)")
         self.row_start, self.kv_len, self.page_table = row_start, kv_len, page_table

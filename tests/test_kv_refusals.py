@@ -202,3 +202,16 @@ def test_a_rope_table_on_the_host_is_refused_by_every_call():
                lambda: plan.decode(b, t, t, rope=table)):
         with pytest.raises(ValueError, match="host"):
             fn()
+
+
+def test_the_python_descriptors_refuse_other_types_of_the_same_size():
+    codes, scales = torch.zeros(4, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2)
+    signed, ints = codes.to(torch.int8), torch.zeros(4, 2, dtype=torch.int32)
+    for bad in ((signed, codes, scales, scales), (codes, signed, scales, scales), (codes, codes.bool(), scales, scales),
+                (codes, codes, ints, scales), (codes, codes, scales, ints)):
+        with pytest.raises(ValueError):
+            mq.KVCache(*bad)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    for bad in ((i(3).to(torch.uint32), i(2), i(2, 4)), (i(3), i(2).to(torch.uint32), i(2, 4)), (i(3), i(2), i(2, 4).view(torch.uint32))):
+        with pytest.raises(ValueError):
+            mq.KVBatch(*bad, 2, 1, 8)
