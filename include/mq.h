@@ -399,12 +399,13 @@ typedef struct mq_kv_cache {
  * that captured a call replays with whatever they hold then. A sequence that
  * does not keep the bounds, or a page number outside [0, n_pages), touches no
  * memory: mq_device_status() reports MQ_ERR_BOUNDS and the outputs of that
- * sequence are undefined.
+ * sequence are undefined. With n_seqs, n_rows or max_new 0 a call does nothing,
+ * and its row buffers may be NULL (empty tensors).
  */
 typedef struct mq_kv_batch {
   const int32_t* row_start;  /* n_seqs + 1, not decreasing, row_start[0] >= 0 */
   const int32_t* kv_len;     /* n_seqs */
-  const int32_t* page_table; /* n_seqs x max_pages */
+  const int32_t* page_table; /* n_seqs x max_pages (NULL where max_pages is 0) */
   int64_t n_seqs;            /* at most 65535; 0 does nothing */
   int64_t max_pages;         /* row pitch of page_table */
   int64_t n_rows;

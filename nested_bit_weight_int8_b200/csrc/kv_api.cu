@@ -71,7 +71,7 @@ mq_status check_batch(const char* who, const mq_kv_batch* b, const KvCache& c, K
     return refuse(MQ_ERR_INVALID_ARG, "%s: negative size in the batch", who);
   *empty = b->n_seqs == 0;
   if (*empty) return MQ_OK;
-  if (!b->row_start || !b->kv_len || !b->page_table) return refuse(MQ_ERR_INVALID_ARG, "%s: null pointer in the batch", who);
+  if (!b->row_start || !b->kv_len || (!b->page_table && b->max_pages > 0)) return refuse(MQ_ERR_INVALID_ARG, "%s: null pointer in the batch", who);
   if (!on(b->row_start, 4) || !on(b->kv_len, 4) || !on(b->page_table, 4))
     return refuse(MQ_ERR_INVALID_ARG, "%s: the batch's arrays must be 4-byte aligned", who);
   if (b->n_seqs > 65535 || b->n_rows > (1 << 28) || b->max_new > (1 << 28) || b->max_pages > (1 << 26) || b->max_len > (1 << 30))
@@ -84,9 +84,10 @@ mq_status check_batch(const char* who, const mq_kv_batch* b, const KvCache& c, K
   return MQ_OK;
 }
 
-// A row of `heads` heads inside a stride, for runs of `run` elements.
-mq_status check_rows(const char* who, const char* what, const void* p, int64_t stride, int64_t width, int item, int run) {
-  if (!p) return refuse(MQ_ERR_INVALID_ARG, "%s: null %s", who, what);
+// A row of `heads` heads inside a stride, for runs of `run` elements. none: there is no row
+// (an empty tensor's address is null).
+mq_status check_rows(const char* who, const char* what, const void* p, int64_t stride, int64_t width, int item, int run, bool none) {
+  if (!p && !none) return refuse(MQ_ERR_INVALID_ARG, "%s: null %s", who, what);
   if (!on(p, run * item)) return refuse(MQ_ERR_INVALID_ARG, "%s: %s must be %d-byte aligned", who, what, run * item);
   if (stride < width || stride % run != 0)
     return refuse(MQ_ERR_INVALID_ARG, "%s: the row stride of %s must be a multiple of %d, at least %lld", who, what, run,
@@ -116,21 +117,21 @@ mq_status kv_append_args(const char* who, const mq_kv_cache* cache, const mq_kv_
   if (st != MQ_OK) return st;
   if ((st = check_batch(who, batch, a.c, &a.b, &empty)) != MQ_OK) return st;
   if (!is_dtype(dtype)) return refuse(MQ_ERR_INVALID_ARG, "%s: dtype must be MQ_F32 or MQ_BF16", who);
+  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
   const int item = dtype == MQ_F32 ? 4 : 2;
   const int64_t width = int64_t(a.c.heads) * a.c.d;
-  if ((st = check_rows(who, "k", k, k_stride, width, item, 4)) != MQ_OK) return st;
-  if ((st = check_rows(who, "v", v, v_stride, width, item, 4)) != MQ_OK) return st;
+  if ((st = check_rows(who, "k", k, k_stride, width, item, 4, *nothing)) != MQ_OK) return st;
+  if ((st = check_rows(who, "v", v, v_stride, width, item, 4, *nothing)) != MQ_OK) return st;
   if (rope && (st = check_rope(who, rope, a.c.d, 8, &a.rope)) != MQ_OK) return st;
   if (!on(positions, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: positions must be 4-byte aligned", who);
   if (positions && !rope) return refuse(MQ_ERR_INVALID_ARG, "%s: positions without rope", who);
   if (q) {
     if (n_q_heads < 1 || n_q_heads > 65535) return refuse(MQ_ERR_INVALID_ARG, "%s: n_q_heads must be in [1, 65535]", who);
-    if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, item, 4)) != MQ_OK) return st;
+    if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, item, 4, false)) != MQ_OK) return st;
     if (!q_out || !on(q_out, 8)) return refuse(MQ_ERR_INVALID_ARG, "%s: q_out null or not 8-byte aligned", who);
   } else if (q_out) {
     return refuse(MQ_ERR_INVALID_ARG, "%s: q_out without q", who);
   }
-  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
   if (*nothing) return MQ_OK;
   a.k = k;
   a.v = v;
@@ -158,11 +159,11 @@ mq_status kv_attention_args(const char* who, const mq_kv_cache* cache, const mq_
   if (!(softcap == 0.f || (softcap >= 0x1p-60f && softcap <= 0x1p60f)))
     return refuse(MQ_ERR_INVALID_ARG, "%s: softcap must be 0 (none) or in [2^-60, 2^60]", who);
   if (window < 0) return refuse(MQ_ERR_INVALID_ARG, "%s: window must be >= 0 (0: none)", who);
-  if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
-  if ((st = check_rows(who, "out", out, out_stride, n_q_heads * a.c.d, 2, 8)) != MQ_OK) return st;
+  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
+  if ((st = check_rows(who, "q", q, q_stride, n_q_heads * a.c.d, 2, 8, *nothing)) != MQ_OK) return st;
+  if ((st = check_rows(who, "out", out, out_stride, n_q_heads * a.c.d, 2, 8, *nothing)) != MQ_OK) return st;
   if (!on(lse, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", who);
   if (!scratch || !on(scratch, 256)) return refuse(MQ_ERR_INVALID_ARG, "%s: scratch null or not 256-byte aligned", who);
-  *nothing = empty || a.b.n_rows == 0 || a.b.max_new == 0;
   if (*nothing) return MQ_OK;
   const int sms = sm_count();
   if (scratch_bytes < kv_attention_scratch(a.c, a.b, a.group, sms))
@@ -241,11 +242,11 @@ mq_status mq_rope(const void* x, int x_dtype, int64_t n_rows, int64_t n_heads, i
   Rope r{};
   mq_status st = check_rope(who, rope, head_dim, 2, &r);
   if (st != MQ_OK) return st;
-  if ((st = check_rows(who, "x", x, x_stride, n_heads * head_dim, x_dtype == MQ_F32 ? 4 : 2, 1)) != MQ_OK) return st;
-  if ((st = check_rows(who, "y", y, y_stride, n_heads * head_dim, y_dtype == MQ_F32 ? 4 : 2, 1)) != MQ_OK) return st;
-  if (x == y && (x_dtype != y_dtype || x_stride != y_stride))
+  if ((st = check_rows(who, "x", x, x_stride, n_heads * head_dim, x_dtype == MQ_F32 ? 4 : 2, 1, n_rows == 0)) != MQ_OK) return st;
+  if ((st = check_rows(who, "y", y, y_stride, n_heads * head_dim, y_dtype == MQ_F32 ? 4 : 2, 1, n_rows == 0)) != MQ_OK) return st;
+  if (x && x == y && (x_dtype != y_dtype || x_stride != y_stride))
     return refuse(MQ_ERR_INVALID_ARG, "%s: in place needs one type and one stride", who);
-  if (!positions || !on(positions, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: positions null or not 4-byte aligned", who);
+  if ((!positions && n_rows > 0) || !on(positions, 4)) return refuse(MQ_ERR_INVALID_ARG, "%s: positions null or not 4-byte aligned", who);
   if (n_rows == 0) return MQ_OK;
   return finish(launch_rope(x, x_dtype, n_rows, static_cast<int>(n_heads), static_cast<int>(head_dim), x_stride, positions, r, y,
                             y_dtype, y_stride, static_cast<cudaStream_t>(stream), sm_count()), who);
@@ -285,8 +286,8 @@ mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const i
     return refuse(MQ_ERR_INVALID_ARG, "%s: first / out_start null or not 4-byte aligned", who);
   const int item = dtype == MQ_F32 ? 4 : 2;
   const int64_t width = int64_t(a.c.heads) * a.c.d;
-  if ((st = check_rows(who, "k_out", k_out, out_stride, width, item, 16 / item)) != MQ_OK) return st;
-  if ((st = check_rows(who, "v_out", v_out, out_stride, width, item, 16 / item)) != MQ_OK) return st;
+  if ((st = check_rows(who, "k_out", k_out, out_stride, width, item, 16 / item, false)) != MQ_OK) return st;
+  if ((st = check_rows(who, "v_out", v_out, out_stride, width, item, 16 / item, false)) != MQ_OK) return st;
   a.first = first;
   a.out_start = out_start;
   a.n_out = static_cast<int>(n_out);

@@ -85,3 +85,38 @@ def test_read_back_of_more_rows_than_max_out_is_reported():
     with pytest.raises(mq.MQError) as e:
         mq.device_status()
     assert e.value.status == mq.MQ_ERR_BOUNDS and torch.all(k == 5.0) and torch.all(v == 5.0)
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_idle_sequences_need_no_pages(rows):
+    # a page table of no columns: nothing is written, every row attends to nothing
+    heads, dim = 2, 64
+    b = Batch([(1, 20)], heads, dim, 16, seed=4)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    batch = mq.KVBatch(torch.tensor([0, rows, rows + 1], **i32), torch.zeros(2, **i32), torch.empty(2, 0, **i32), rows + 1, rows, 0)
+    x = torch.randn(rows + 1, heads * dim, device=DEV)
+    mq.kv_append(b.cache, batch, x, x, mq.MQ_F32, heads * dim, heads * dim)
+    q = x.to(torch.bfloat16)
+    out, lse = torch.full_like(q, 9.0), torch.full((rows + 1, heads), 9.0, device=DEV)
+    scratch = torch.empty(mq.kv_attention_scratch_bytes(b.cache, batch, heads), dtype=torch.uint8, device=DEV)
+    mq.kv_attention(b.cache, batch, q, heads * dim, heads, 0.1, out, heads * dim, scratch, lse=lse)
+    mq.device_status()
+    assert torch.all(out == 0) and torch.all(lse == -torch.inf)
+    for which in range(2):
+        codes, scales = b.host(which)
+        assert np.array_equal(codes, b.codes[which]) and np.array_equal(scales, b.scales[which])
+
+
+def test_calls_on_empty_tensors_do_nothing():
+    b = Batch([(1, 20)], 2, 64, 16, seed=4)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    batch = mq.KVBatch(torch.zeros(2, **i32), torch.zeros(1, **i32), b.pages, 0, 0, 20)
+    x, q = torch.empty(0, 128, device=DEV), torch.empty(0, 128, device=DEV, dtype=torch.bfloat16)
+    mq.kv_append(b.cache, batch, x, x, mq.MQ_F32, 128, 128, q=x, q_stride=128, n_q_heads=2, q_out=q)
+    scratch = torch.empty(mq.kv_attention_scratch_bytes(b.cache, batch, 2), dtype=torch.uint8, device=DEV)
+    mq.kv_attention(b.cache, batch, q, 128, 2, 0.1, q, 128, scratch)
+    mq.rope(x, mq.MQ_F32, 0, 2, 64, 128, torch.empty(0, **i32), mq.RopeTable(1e4, 64, device=DEV), x, mq.MQ_F32, 128)
+    mq.device_status()
+    for which in range(2):
+        codes, scales = b.host(which)
+        assert np.array_equal(codes, b.codes[which]) and np.array_equal(scales, b.scales[which])

@@ -215,3 +215,20 @@ def test_the_python_descriptors_refuse_other_types_of_the_same_size():
     for bad in ((i(3).to(torch.uint32), i(2), i(2, 4)), (i(3), i(2).to(torch.uint32), i(2, 4)), (i(3), i(2), i(2, 4).view(torch.uint32))):
         with pytest.raises(ValueError):
             mq.KVBatch(*bad, 2, 1, 8)
+
+
+def test_calls_without_rows_take_empty_tensors():
+    # an empty tensor's address is null; sizes and types are looked at all the same
+    for kw in (dict(n_seqs=0, row_start=None, kv_len=None, page_table=None, n_rows=0), dict(n_rows=0)):
+        b = batch(**kw)
+        assert call(mq._kv_append, APPEND, b=b, k=None, v=None, q=None, qo=None) == mq.MQ_OK
+        assert call(mq._kv_attention, ATTEND, b=b, q=None, out=None) == mq.MQ_OK
+        assert call(mq._kv_append, APPEND, b=b, k=None, v=None, q=None, qo=None, ks=255) == BAD
+        assert call(mq._kv_attention, ATTEND, b=b, q=None, out=None, os=1000) == BAD
+    assert call(mq._rope, ROPE, rows=0, x=None, y=None, pos=None) == mq.MQ_OK
+    assert call(mq._rope, ROPE, rows=0, x=None, y=None, pos=None, xs=255) == BAD
+    # sequences that hold nothing need no pages
+    idle = batch(max_pages=0, max_len=0, page_table=None, n_rows=0)
+    assert call(mq._kv_append, APPEND, b=idle) == mq.MQ_OK
+    assert call(mq._kv_attention, ATTEND, b=batch(max_pages=0, max_len=0, page_table=None), scr=None) == BAD
+    assert "scratch" in mq.last_error()
