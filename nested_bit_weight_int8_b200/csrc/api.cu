@@ -141,6 +141,10 @@ uint32_t* find_error_word() {
 uint64_t wait_limit_ns() { return g_wait_limit_ns; }
 
 void set_last_error(const char* msg) { g_last_error = msg; }
+mq_status out_of_memory() {
+  g_last_error = "no host memory";  // short enough to need none
+  return MQ_ERR_CUDA;
+}
 
 }  // namespace mq
 
@@ -409,7 +413,7 @@ size_t mq_chain_decode_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch
 
 mq_status mq_chain_decode(const mq_chain_layer* layers, const mq_kv_cache* caches, int n_layers, const mq_kv_batch* batch,
                           const mq_rope_positions* rope, float softcap, int64_t window, int64_t D, int64_t Dkv, int64_t F, float* h,
-                          void* scratch, size_t scratch_bytes, int flags, void* stream) {
+                          void* scratch, size_t scratch_bytes, int flags, void* stream) try {
   TraceRange trace_("mq_chain_decode");
   g_last_error.clear();
   const char* who = "mq_chain_decode";
@@ -449,6 +453,8 @@ mq_status mq_chain_decode(const mq_chain_layer* layers, const mq_kv_cache* cache
                             static_cast<cudaStream_t>(stream), &cached);
   if (e != cudaSuccess) return cuda_fail(e, who);
   return MQ_OK;
+} catch (...) {
+  return out_of_memory();
 }
 
 mq_status mq_container_save(const char* path, const uint8_t* q, const float* alpha, const float* zero,

@@ -186,7 +186,7 @@ using namespace mq;
 
 extern "C" {
 
-mq_status mq_rope_table(double theta, int rot_dim, int scaling, const double* params, uint64_t* turns, float* factor) {
+mq_status mq_rope_table(double theta, int rot_dim, int scaling, const double* params, uint64_t* turns, float* factor) try {
   set_last_error("");
   const char* who = "mq_rope_table";
   if (!turns || !factor) return refuse(MQ_ERR_INVALID_ARG, "%s: null output", who);
@@ -226,11 +226,13 @@ mq_status mq_rope_table(double theta, int rot_dim, int scaling, const double* pa
     turns[i] = f >= 18446744073709551615.0L ? 0 : static_cast<uint64_t>(f + 0.5L);
   }
   return MQ_OK;
+} catch (...) {
+  return out_of_memory();
 }
 
 mq_status mq_rope(const void* x, int x_dtype, int64_t n_rows, int64_t n_heads, int64_t head_dim, int64_t x_stride,
                   const int32_t* positions, const mq_rope_positions* rope, void* y, int y_dtype, int64_t y_stride,
-                  void* stream) {
+                  void* stream) try {
   TraceRange trace_("mq_rope");
   set_last_error("");
   const char* who = "mq_rope";
@@ -250,11 +252,13 @@ mq_status mq_rope(const void* x, int x_dtype, int64_t n_rows, int64_t n_heads, i
   if (n_rows == 0) return MQ_OK;
   return finish(launch_rope(x, x_dtype, n_rows, static_cast<int>(n_heads), static_cast<int>(head_dim), x_stride, positions, r, y,
                             y_dtype, y_stride, static_cast<cudaStream_t>(stream), sm_count()), who);
+} catch (...) {
+  return out_of_memory();
 }
 
 mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* k, const void* v, int dtype,
                        int64_t k_stride, int64_t v_stride, const mq_rope_positions* rope, const int32_t* positions,
-                       const void* q, int64_t q_stride, int64_t n_q_heads, void* q_out, void* stream) {
+                       const void* q, int64_t q_stride, int64_t n_q_heads, void* q_out, void* stream) try {
   TraceRange trace_("mq_kv_append");
   set_last_error("");
   const char* who = "mq_kv_append";
@@ -266,10 +270,12 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
   const cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
   return finish(launch_kv_append(a, dtype, static_cast<cudaStream_t>(stream), sm_count()), who);
+} catch (...) {
+  return out_of_memory();
 }
 
 mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const int32_t* first, const int32_t* out_start,
-                     int64_t n_out, int64_t max_out, void* k_out, void* v_out, int dtype, int64_t out_stride, void* stream) {
+                     int64_t n_out, int64_t max_out, void* k_out, void* v_out, int dtype, int64_t out_stride, void* stream) try {
   TraceRange trace_("mq_kv_read");
   set_last_error("");
   const char* who = "mq_kv_read";
@@ -299,9 +305,11 @@ mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch, const i
   cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
   return finish(launch_kv_read(a, dtype, static_cast<cudaStream_t>(stream)), who);
+} catch (...) {
+  return out_of_memory();
 }
 
-size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch, int64_t n_q_heads) {
+size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch, int64_t n_q_heads) try {
   const char* who = "mq_kv_attention_scratch_bytes";
   set_last_error("");
   KvCache c{};
@@ -312,11 +320,14 @@ size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch
   if (empty) return 256;
   if (check_group(who, c, b, n_q_heads, &group) != MQ_OK) return 0;
   return kv_attention_scratch(c, b, group, sm_count());
+} catch (...) {
+  out_of_memory();
+  return 0;
 }
 
 mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q, int64_t q_stride,
                           int64_t n_q_heads, float scale, float softcap, int64_t window, void* out, int64_t out_stride,
-                          float* lse, void* scratch, size_t scratch_bytes, void* stream) {
+                          float* lse, void* scratch, size_t scratch_bytes, void* stream) try {
   TraceRange trace_("mq_kv_attention");
   set_last_error("");
   const char* who = "mq_kv_attention";
@@ -328,6 +339,8 @@ mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, co
   const cudaError_t e = get_error_word(&a.err);
   if (e != cudaSuccess) return finish(e, who);
   return finish(launch_kv_attention(a, static_cast<cudaStream_t>(stream), sm_count()), who);
+} catch (...) {
+  return out_of_memory();
 }
 
 }  // extern "C"

@@ -9,6 +9,8 @@
 #include <cstdint>
 #include <vector>
 
+#include "../../include/mq.h"
+
 namespace mq {
 
 // One sliced linear as the host planner sees it (device pointers).
@@ -93,6 +95,9 @@ cudaError_t get_error_word(uint32_t** out);
 uint64_t wait_limit_ns();
 // Replaces the calling thread's mq_last_error() text.
 void set_last_error(const char* msg);
+// What an entry point returns for a C++ exception, none of which may cross it: the
+// library throws none but the standard containers'.
+mq_status out_of_memory();
 
 // 2-D tensor map over a row-major matrix of `rows` x `row_elems` elements of
 // `elem_bytes` bytes (1: uint8, 2: bf16), box `box_inner` x `box_rows`,

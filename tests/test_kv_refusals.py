@@ -2,6 +2,8 @@
 refusal happens on the host, before a launch (no GPU needed)."""
 import ctypes
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -232,3 +234,24 @@ def test_calls_without_rows_take_empty_tensors():
     assert call(mq._kv_append, APPEND, b=idle) == mq.MQ_OK
     assert call(mq._kv_attention, ATTEND, b=batch(max_pages=0, max_len=0, page_table=None), scr=None) == BAD
     assert "scratch" in mq.last_error()
+
+
+def test_a_chain_that_finds_no_host_memory_reports_it():
+    # the launch arguments of so many layers take some 20 MB; the process may have 4 MB more
+    script = f"""
+import ctypes, os, resource, sys
+sys.path[:0] = {sys.path[:4]!r}
+import nested_bit_weight_int8_b200 as mq
+from test_kv_refusals import CHAIN, cache, chain_layer
+n = 1 << 16
+layers, caches = (mq.ChainLayer * n)(*[chain_layer()] * n), (mq.KVCacheDesc * n)(*[cache()] * n)
+args = list({{**CHAIN, "layers": layers, "caches": caches, "n": n}}.values())
+now = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (now + (4 << 20), resource.RLIM_INFINITY))
+status = mq._chain_decode(*args)
+os.write(1, b"%d " % status + mq._last_error())
+os._exit(0)
+"""
+    got = subprocess.run([sys.executable, "-c", script], capture_output=True, timeout=300)
+    assert got.returncode == 0, got.stderr[-500:]
+    assert got.stdout.decode() == f"{mq.MQ_ERR_CUDA} no host memory"
