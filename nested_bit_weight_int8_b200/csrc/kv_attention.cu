@@ -293,7 +293,6 @@ struct Worker {
 
     float o[NR][kMt][4];
     float m[NR][2], l[NR][2], vmax = kTinyScale, vinv = kPScale / kTinyScale;
-    bool coarse = false;  // some row has a maximum beyond kCoarse
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       m[r][0] = m[r][1] = -INFINITY;
@@ -304,7 +303,7 @@ struct Worker {
         for (int e = 0; e < 4; ++e) o[r][i][e] = 0.f;
     }
     // the places of the tile's first and last query token
-    const int lo_place = sq.len - sq.n + it.i0;
+    int lo_place = sq.len - sq.n + it.i0;
     const int hi_place = sq.len - sq.n + (first_row + it.rows - 1) / a.group;
     const float cap_in = a.softcap > 0.f ? 1.f / a.softcap : 0.f, cap_out = a.softcap * kLog2e;
     // where this lane's chunks lie in a box: K rows g ^ ((g & 1) << 2) and + 8, V rows 2 t, (2 t + 1) ^ 4 and + 8
@@ -365,7 +364,7 @@ struct Worker {
       }
       // ---- cap and mask, where there is one; a score (base 2) is then sc f
       const int jt = it.j0 + tile * S::kTile;
-      const bool masked = coarse || dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
+      const bool masked = dead || jt + S::kTile - 1 > lo_place || (a.window > 0 && jt <= hi_place - a.window);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -441,8 +440,8 @@ struct Worker {
             for (int i = 0; i < kMt; ++i) o[r][i][e] *= kv, o[r][i][2 + e] *= kv;
           }
         }
-        coarse = __any_sync(0xffffffffu, far);
-        if (coarse) {
+        if (__any_sync(0xffffffffu, far)) {  // the tiles to come go the way of the masked ones
+          lo_place = -1;
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
 #pragma unroll

@@ -434,12 +434,12 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
     }
     // of the 32 rows of this warp
     const int first_row = w.row0 + 128 * mt + 32 * (warp & 3);
-    const int w_lo = w.past + first_row / a.group, w_hi = w.past + min(first_row + 31, w.all - 1) / a.group;
+    int w_lo = w.past + first_row / a.group;
+    const int w_hi = w.past + min(first_row + 31, w.all - 1) / a.group;
     // Rows behind the sequence's last (zero queries) keep a maximum of -infinity, which keeps
     // their sums out; what they get in P and O is finite and goes nowhere. A warp of them does nothing.
     const bool idle = first_row >= w.all;
     float m = -INFINITY, l = 0.f, vmax = kTinyScale;
-    bool coarse = false;  // some row of this warp has a maximum beyond kCoarse
     // A tile's scales (K's times this row's factor), taken while its scores are still being
     // made: the products keep shared memory busy, and a load waits for hundreds of cycles.
     float fs[P::kGroups], lg[P::kGroups], tile_vmax = 0.f;
@@ -464,7 +464,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       tc05::fence_after_sync();
       const uint32_t t_s = tmem + lanes + slot * kT;
       const int jt = w.j0 + i * kT;
-      const bool special = a.softcap > 0.f || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
+      bool special = a.softcap > 0.f || dead || jt + kT - 1 > w_lo || (a.window > 0 && jt <= w_hi - a.window);
       const float2* group_scales = s_scales[tick % P::kSlots].group;
       auto factor = [&](int g) { return fac * group_scales[g].x; };
       // The scores of groups g, g + 1, scaled, and where some row of the warp needs it capped and masked.
@@ -511,7 +511,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         l *= k;
         sum *= k;
         m = x;
-        coarse = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m) >= kCoarse);
+        if (__any_sync(0xffffffffu, m != -INFINITY && fabsf(m) >= kCoarse)) special = true, w_lo = -1;  // from here on
         vmax = tile_vmax;
         const __half2 k2 = __float2half2_rn(k);
         tc05::wait_st();  // P so far
@@ -556,15 +556,14 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       // leave 2^-126 of what is masked).
       // A step is done over once at most: the maximum is then at least that of its own scores
       // and no p' stands above 2^8 (but for the roundings below kCoarse), no group's sum above
-      // 2^12. Tiles with a maximum beyond kCoarse go the way of the masked ones, to their end.
+      // 2^12. From a maximum beyond kCoarse on, the piece goes the way of the masked tiles.
       const bool first = __any_sync(0xffffffffu, live && m == -INFINITY);
-      bool rise = first || tile_vmax != vmax, enough = true, careful = special || coarse;
+      bool rise = first || tile_vmax != vmax, enough = true;
       int g0 = idle ? P::kGroups : 0, seek_to = first ? P::kGroups : 0;  // where a maximum is looked for ends
       while (g0 < P::kGroups) {
         if (rise) {
           if (!(ok = raise(largest(g0, seek_to, enough), 8 * g0))) break;
           rise = false;
-          careful |= coarse;
         }
         const float m0 = m == -INFINITY ? 0.f : m;
         float part = 0.f, big = 0.f, over = 0.f;
@@ -588,7 +587,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           part = fmaf(t.x + t.y, exp2_fast(-lg), part);
         };
         int step;
-        if (!careful) {
+        if (!special) {
           step = 4;
           uint32_t v[2][32], pk[32];
           tc05::ld_32x32b_x32(t_s + 16 * g0, v[0]);
