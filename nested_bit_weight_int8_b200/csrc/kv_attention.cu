@@ -196,7 +196,7 @@ struct Worker {
             mine = make_float2(0.f, -1.f);
             if (pid >= 0) {
               const int64_t at = int64_t(pid) * a.c.heads + h;
-              mine = make_float2(__ldg(a.c.k_scale + at), __ldg(a.c.v_scale + at));
+              mine = make_float2(a.c.k_scale[at], a.c.v_scale[at]);
             }
           }
           if (lane == index - page0) {
@@ -230,7 +230,7 @@ struct Worker {
         const bool in = lr < it.rows && c < chunks;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          raw[r][j][k] = in ? __ldg(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
+          raw[r][j][k] = in ? *(reinterpret_cast<const uint4*>(qp + 16 * c) + k) : make_uint4(0, 0, 0, 0);
       }
     }
     const int stage0 = ring.stage;

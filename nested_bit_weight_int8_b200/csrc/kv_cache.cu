@@ -56,10 +56,10 @@ __device__ __forceinline__ void turn_sincos(uint64_t phase, float& sn, float& cs
 template <typename T, int V>
 __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
   if constexpr (V == 4 && sizeof(T) == 4) {
-    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 u = *reinterpret_cast<const float4*>(p);
     v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
   } else if constexpr (V == 4) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
     v[0] = __uint_as_float(u.x << 16);
     v[1] = __uint_as_float(u.x & 0xFFFF0000u);
     v[2] = __uint_as_float(u.y << 16);
@@ -144,7 +144,7 @@ constexpr int kRopeThreads = 256;
 // x. V = 4 needs rot and d in eights and aligned runs; V = 1 takes the rest.
 template <typename TI, typename TO, int V>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_kernel(const TI* x, int64_t rows, int heads, int d, int64_t x_stride, const int32_t* __restrict__ positions,
+rope_kernel(const TI* x, int64_t rows, int heads, int d, int64_t x_stride, const int32_t* positions,
             Rope rope, TO* y, int64_t y_stride, int units, int head_lanes, int head_splits) {
   pdl_launch_dependents();
   pdl_wait_primary();

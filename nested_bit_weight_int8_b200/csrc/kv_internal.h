@@ -118,6 +118,10 @@ mq_status kv_attention_args(const char* who, const mq_kv_cache* cache, const mq_
                             void* scratch, size_t scratch_bytes, AttendArgs* out_args, bool* nothing);
 
 #ifdef __CUDACC__
+// These kernels may be resident while the one before them still writes what they read: they
+// wait for it (pdl_wait_primary), and read with plain loads. The read-only path (__ldg, const
+// __restrict__) is for memory that nothing writes while a kernel lives.
+//
 // A sequence of the batch: its first row, its rows and its tokens. A sequence
 // whose numbers do not fit the call (rows outside [0, n_rows), more rows than
 // max_new, more tokens than max_len) is flagged and has no rows.

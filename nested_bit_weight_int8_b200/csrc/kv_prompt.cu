@@ -405,7 +405,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int64_t at = __shfl_sync(0xffffffffu, from, (k0 + k) * kRowsAt + sub);
-          u[k] = at >= 0 && chunk < 2 * chunks ? __ldg(reinterpret_cast<const uint4*>(a.q + at) + chunk) : make_uint4(0, 0, 0, 0);
+          u[k] = at >= 0 && chunk < 2 * chunks ? *(reinterpret_cast<const uint4*>(a.q + at) + chunk) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
@@ -733,7 +733,7 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
       const int64_t tl = int64_t(pid) * a.c.heads + w.h;
       const int64_t group = pid < 0 ? -1 : (tl * page + ((w.j0 + i * kT + 16 * lane) & (page - 1))) * d;
       sc = make_float2(0.f, 0.f);
-      if (pid >= 0) sc = make_float2(__ldg(a.c.k_scale + tl), __ldg(a.c.v_scale + tl));
+      if (pid >= 0) sc = make_float2(a.c.k_scale[tl], a.c.v_scale[tl]);
 #pragma unroll
       for (int k = 0; k < kIt; ++k) {
         const int first = cw * kTokens + k * kAt;  // token of the tile

@@ -120,3 +120,46 @@ def test_calls_on_empty_tensors_do_nothing():
     for which in range(2):
         codes, scales = b.host(which)
         assert np.array_equal(codes, b.codes[which]) and np.array_equal(scales, b.scales[which])
+
+
+def test_calls_back_to_back_read_what_the_call_before_wrote():
+    # each kernel may start beside the one before it: queries, codes and scales that change with every
+    # call, the neighbours' scales in the same lines among them, bit for bit as with a wait between the calls
+    heads, group, dim, page, seqs = 8, 4, 64, 16, 24
+    hq, pitch = heads * group, (heads * group + 2 * heads) * dim
+    i32 = dict(dtype=torch.int32, device=DEV)
+    rows = 3 * seqs
+    starts = torch.arange(0, rows + 1, 3, **i32)
+    tables = torch.randperm(seqs * 8, generator=torch.Generator().manual_seed(0)).view(seqs, 8).to(**i32)
+    table = mq.RopeTable(10000.0, dim, device=DEV)
+    positions, back = (torch.full((rows,), p, **i32) for p in (3, -3))
+
+    def run(wait):
+        gen = torch.Generator(device=DEV).manual_seed(1)
+        pool = [torch.full((seqs * 8, heads, page, dim), 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        cache = mq.KVCache(*pool, *(torch.zeros(seqs * 8, heads, device=DEV) for _ in range(2)))
+        kv_len = torch.zeros(seqs, **i32)
+        batch = mq.KVBatch(starts, kv_len, tables, rows, 3, 128)
+        scratch = torch.empty(mq.kv_attention_scratch_bytes(cache, batch, hq), dtype=torch.uint8, device=DEV)
+        x = [torch.randn(rows, pitch, device=DEV, generator=gen) * (1 + step) for step in range(40)]  # scales grow each time
+        y, q, out = torch.empty(rows, pitch, device=DEV), torch.empty(rows, hq * dim, device=DEV, dtype=torch.bfloat16), []
+        first, ends = torch.zeros(seqs, **i32), torch.arange(0, seqs * 4 + 1, 4, **i32)
+        for step in range(40):
+            kv_len += 3
+            got = [torch.empty(rows, hq * dim, device=DEV, dtype=torch.bfloat16), *(torch.empty(seqs * 4, heads * dim, device=DEV) for _ in range(2))]
+            for call in (lambda: mq.rope(x[step], mq.MQ_F32, rows, pitch // dim, dim, pitch, positions, table, y, mq.MQ_F32, pitch),
+                         lambda: mq.rope(y, mq.MQ_F32, rows, pitch // dim, dim, pitch, back, table, y, mq.MQ_F32, pitch),
+                         lambda: mq.kv_append(cache, batch, y[:, hq * dim:], y[:, (hq + heads) * dim:], mq.MQ_F32, pitch, pitch,
+                                              rope=table, q=y, q_stride=pitch, n_q_heads=hq, q_out=q),
+                         lambda: mq.kv_attention(cache, batch, q, hq * dim, hq, dim ** -0.5, got[0], hq * dim, scratch),
+                         lambda: mq.kv_read(cache, batch, first, ends, seqs * 4, 4, got[1], got[2], mq.MQ_F32, heads * dim)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            out.append(got)
+        mq.device_status()
+        return out
+
+    for a, b in zip(run(True), run(False)):
+        for u, v in zip(a, b):
+            assert torch.equal(u, v)
