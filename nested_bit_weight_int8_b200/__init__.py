@@ -275,7 +275,7 @@ class ChainPlan:
         (n_rows x D fp32) in place. scratch: decode_scratch_bytes."""
         if self.caches is None:
             raise ValueError("the plan has no caches")
-        _check(_chain_decode(self.arr, self.cache_arr, self.n, batch.desc, _table(rope),
+        _check(_chain_decode(self.arr, self.cache_arr, self.n, batch.desc, rope.desc if rope is not None else None,
                              softcap, window, self.D, self.Dkv, self.F, _ptr(h), _ptr(scratch),
                              scratch.numel() * scratch.element_size(), MQ_CHAIN_GRAPH if graph else 0, _stream(stream)))
 
@@ -307,15 +307,13 @@ class RopeTable:
                            ctypes.byref(factor)))
         self.turns = host if device is None else host.to(device)
         self.factor = factor.value
-        self.desc = RopePositions(self.turns.data_ptr(), rot_dim, ROPE_LAYOUTS[layout], factor.value)
+        if self.turns.is_cuda:
+            self.desc = RopePositions(self.turns.data_ptr(), rot_dim, ROPE_LAYOUTS[layout], factor.value)
 
-
-def _table(rope: RopeTable | None):
-    if rope is None:
-        return None
-    if not rope.turns.is_cuda:
-        raise ValueError("the rope table lies on the host: give RopeTable a CUDA device")
-    return rope.desc
+    def __getattr__(self, name):  # what __init__ did not set
+        if name == "desc":
+            raise ValueError("the rope table lies on the host: give RopeTable a CUDA device")
+        raise AttributeError(name)
 
 
 class KVCache:
@@ -356,7 +354,7 @@ class KVBatch:
 def rope(x, x_dtype: int, n_rows: int, n_heads: int, head_dim: int, x_stride: int, positions, table: RopeTable,
          y, y_dtype: int, y_stride: int, stream=None) -> None:
     """Rotary positions of n_rows x n_heads heads; y may be x. Strides in elements."""
-    _check(_rope(_ptr(x), x_dtype, n_rows, n_heads, head_dim, x_stride, _ptr(positions), _table(table), _ptr(y),
+    _check(_rope(_ptr(x), x_dtype, n_rows, n_heads, head_dim, x_stride, _ptr(positions), table.desc, _ptr(y),
                  y_dtype, y_stride, _stream(stream)))
 
 
@@ -366,7 +364,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, dtype: int, k_stride: int, v
     """Quantises the batch's new keys (rotated) and values into the cache, and
     writes their rotated queries to q_out (bf16) if q is given."""
     _check(_kv_append(cache.desc, batch.desc, _ptr(k), _ptr(v), dtype, k_stride, v_stride,
-                      _table(rope), _ptr(positions), _ptr(q), q_stride, n_q_heads,
+                      rope.desc if rope is not None else None, _ptr(positions), _ptr(q), q_stride, n_q_heads,
                       _ptr(q_out), _stream(stream)))
 
 
