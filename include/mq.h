@@ -430,8 +430,8 @@ typedef struct mq_kv_batch {
  *   positions : n_rows int32, or NULL: each row's place in its sequence.
  *   q    : NULL, or n_rows x n_q_heads x head_dim like k; q_out then receives
  *          the rotated queries as bf16, dense, 8-byte aligned.
- * No page may be written for two sequences of one call; a page that sequences
- * share (a common prefix) must be full.
+ * No page may be written twice in one call (for two sequences, or under two
+ * entries of one); a page that sequences share (a common prefix) must be full.
  */
 MQ_API mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* k,
                               const void* v, int dtype, int64_t k_stride, int64_t v_stride,
@@ -469,8 +469,12 @@ MQ_API mq_status mq_kv_read(const mq_kv_cache* cache, const mq_kv_batch* batch,
  *            the caller; calls that overlap on the GPU need one each. It need
  *            not be cleared and keeps nothing for the next call.
  * Any number of rows: single tokens, drafted tokens and prompts may share a
- * call. fp32 sums and statistics; probabilities are rounded to fp16 before
- * they weigh V. Results do not depend on timing.
+ * call. fp32 sums and statistics, exponentials within 2^-21. Two things are
+ * rounded to fp16: probabilities times their page's V scale, relative to the
+ * largest such scale that the row's tile has met, before they weigh V's codes
+ * (below 2^-22 of it they lose bits); and queries, relative to the largest of
+ * their row (bf16 values below 2^-14 of it lose bits, below 2^-25 all of them).
+ * Results do not depend on timing.
  */
 MQ_API size_t mq_kv_attention_scratch_bytes(const mq_kv_cache* cache, const mq_kv_batch* batch,
                                             int64_t n_q_heads);

@@ -12,8 +12,8 @@
 // of shared memory (TMA boxes of 16 tokens, swizzled), with no barrier between
 // warps. Pieces of an item are joined within the CTA first, then, by a second
 // kernel, over the CTAs; always in their order, so results do not depend on
-// timing. Bound by the bytes: 64 sequences of up to 8192 tokens (676 MB) take 122 us,
-// 84% of what a copy reaches; the rest is the start of a launch and the spread of the
+// timing. Bound by the bytes: 64 sequences of up to 8192 tokens (676 MB) take 122 to 130
+// us (two cards), 84% to 79% of what a copy reaches; the rest is the start of a launch and the spread of the
 // warps' ends.
 //
 // Arithmetic: S^T = K Q^T and O^T = V^T P^T in m16n8k16 products with fp32 sums,

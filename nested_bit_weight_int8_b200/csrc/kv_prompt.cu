@@ -16,9 +16,13 @@
 //   one warp             : issues the products
 //   one warp             : plans the CTA's pieces of items ahead of the others
 // 2048 tokens upon as many cached ones of two sequences, 32 query and 8 key/value heads
-// of 128 values: 264 us, 780 TFLOP/s of the pairs that count (11.3 ms in plain torch). A
-// tile of 128 tokens and 256 rows takes 4000 cycles, its products 2100, its softmax 2700:
-// they overlap in part, one row tile's softmax beside the other's products.
+// of 128 values: 272 to 275 us, 750 TFLOP/s of the pairs that count (11.3 ms in plain
+// torch). Of a CTA's 440000 cycles 81 unmasked tiles (256 rows, 128 tokens) take some 4450
+// each: 2950 of softmax, the rest waiting for the scores (products: 2048 at the tensor
+// cores' rate) and the scales; 3.5 masked ones 6300 of softmax; 4.3 pieces 6000 each for
+// their queries and 5900 for their outputs; the start 5000.
+// Beside kv_attention.cu's roundings (queries and probabilities in fp16, the latter with
+// their page's V scale), a quarter of the exponentials are a polynomial, within 2^-22.
 // The codes enter exactly (byte - 128), the page scales where a row's thread needs
 // them: K's multiplies the score, V's goes into the exponent, so that it costs
 // no instruction per score: p' = 2^(s + log2(v_scale / v_max) + 8 - m), and the sum
