@@ -517,7 +517,6 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
         m = x;
         if (__any_sync(0xffffffffu, m != -INFINITY && fabsf(m) >= kCoarse)) special = true, w_lo = -1;  // from here on
         vmax = tile_vmax;
-        const __half2 k2 = __float2half2_rn(k);
         tc05::wait_st();  // P so far
 #pragma unroll 1
         for (int c = 0; c < done; c += 8) {
@@ -525,9 +524,9 @@ kv_prompt_kernel(const AttendArgs a, const Scratch scr, int limit, uint64_t wait
           tc05::ld_32x32b_x8(t_s + c, v);
           tc05::wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v[e]), k2);
-            v[e] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int e = 0; e < 8; ++e) {  // in fp32: the factor alone may be below what fp16 holds
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+            v[e] = f16x2(y.x * k, y.y * k);
           }
           tc05::st_32x32b_x8(t_s + c, v);
         }

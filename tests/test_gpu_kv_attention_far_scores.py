@@ -171,3 +171,28 @@ def test_a_query_that_is_no_number_gives_no_number(seqs, dim, window):
     mq.device_status()
     assert torch.equal(torch.isnan(log), bad)
     assert torch.equal(torch.isnan(out).view(b.rows, 2, dim), bad[:, :, None].expand(-1, -1, dim))
+
+
+@pytest.mark.parametrize("further", [10, 12, 13, 16, 20])
+@pytest.mark.parametrize("dim,n", [(64, 100), (64, 150), (128, 100), (128, 150), (256, 100)])
+def test_prompts_keep_a_weight_when_a_larger_one_follows_in_its_tile(dim, n, further):
+    # scores (base 2) 0, then 13 (a page whose V scale is 2^-7 of the largest, so that it stays within the
+    # running maximum's slack), then `further` more in the same tile: the second's weight, 2^-further, counts,
+    # as the third's values are small or zero
+    held, seqs = 260, 8
+    for second, third in ((34, 100), (262, 300), (130, 215)):
+        b = Batch([(n, held + n)] * seqs, 1, dim, 16, seed=7, fill="all")
+        rng = np.random.default_rng(further)
+        b.codes[0][:] = b.codes[1][:] = 128
+        b.scales[0][:] = b.scales[1][:] = 1.0
+        for pages in b.table:
+            at, far = (pages[second // 16], 0, second % 16), (pages[third // 16], 0, third % 16)
+            b.codes[0][at], b.codes[0][far] = 128 + 13, 128 + 13 + further
+            b.codes[1][at], b.codes[1][far] = 255, 128 + rng.integers(-9, 10, dim) * rng.integers(0, 2, dim)
+            b.scales[1][at[0]], b.scales[1][far[0]] = 2.0 ** -7, 2.0 ** -14
+        for t, c in ((b.k, b.codes[0]), (b.v, b.codes[1]), (b.ks, b.scales[0]), (b.vs, b.scales[1])):
+            t.copy_(torch.from_numpy(c))
+        q, scale = torch.ones(b.rows, dim, device=DEV, dtype=torch.bfloat16), float(np.float32(np.log(2) / dim))
+        out, log = attend(b, 1, q, scale=scale)
+        mq.device_status()
+        check_far_key(b, q, out, log, scale, 0.0, small=True)
